@@ -362,6 +362,155 @@ int w4a8_linear_prepacked(const float *X, int64_t M, int64_t K, int64_t N,
                           int activation, float *Y, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* ---- Paged key-value cache and the attention that reads it: what a decoder
+ * layer runs between its quantized projections.  A cache holds K and V of
+ * every layer in pages of page_size tokens; a sequence ("slot") owns a row of
+ * a page table and a length:
+ *   k, v     [layers][pages][heads][page_size][head_dim], bf16 bit patterns
+ *            (KV_BF16) or int8 codes (KV_INT8);
+ *   k_scale, v_scale  [layers][pages][heads][page_size] fp32, one scale for
+ *            each token and head (KV_INT8; NULL for KV_BF16): the value is
+ *            code * scale, quantized by the rule of a8_quantize_act with a
+ *            head's vector as the row;
+ *   table    [S][W] int32: entry j of a row is the page of tokens
+ *            j * page_size ... (j + 1) * page_size - 1, -1 where there is none;
+ *   lens     [S] int32, cached tokens; refs [pages] int32, how many rows hold
+ *            the page (0: free).
+ * page_size is a power of two from 16 to 4096 and head_dim a multiple of 16
+ * up to 256, so that 16 consecutive tokens lie in one page and rows are whole
+ * 16-byte pieces in both types (one page is then a contiguous run of every
+ * head's tokens).  1 <= heads <= 65535, layers * pages * heads * page_size *
+ * head_dim <= 2^46, pages < 2^31.  A call takes up to 2^23 rows, forks, slots
+ * or page pairs and up to 2^26 token-head vectors (else W4_ERR_SHAPE).  k, v and the scales are 16-byte aligned.
+ * Values in device memory cannot be checked on the host; the kernels read and
+ * write nothing outside the arrays whatever the tables, lengths and offsets
+ * hold: a table entry outside [0, pages) is no page, a token without a page is
+ * neither written nor attended, lengths are limited to [0, W * page_size].
+ * Slots of pages that hold no token yet may hold anything (NaN included). */
+typedef enum { KV_BF16 = 0, KV_INT8 = 1 } kv_dtype;
+
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t layers, pages, heads, page_size, head_dim;
+    int dtype; /* kv_dtype */
+} kv_cache;
+
+/* Element type of activations around the cache. */
+typedef enum { KV_X_BF16 = 0, KV_X_FP32 = 1 } kv_x_dtype;
+
+/* Write new tokens' K and V into `layer`.  Sequence b's tokens are rows
+ * cu[b] .. cu[b + 1] - 1 of k and v (cu [B + 1] int32, cu[0] = 0, cu[B] = T,
+ * not falling; NULL: row b is sequence b's one token, T = B) and go to
+ * positions start[b], start[b] + 1, ...  A negative start[b], a position
+ * beyond the row and a token without a page are skipped.
+ *   k, v    T rows of [heads][head_dim] values of x_dtype, k_stride / v_stride
+ *           elements from one row to the next (at least heads * head_dim).
+ *   KV_BF16: fp32 values are rounded to bf16 (half to even); KV_INT8: see above.
+ * Two tokens for one place race.  Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE,
+ * W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
+int kv_append(const kv_cache *cache, int64_t layer, const void *k, const void *v, int x_dtype,
+              int64_t k_stride, int64_t v_stride, int64_t T, int64_t B, const int32_t *table,
+              int64_t W, const int32_t *start, const int32_t *cu, void *stream);
+
+/* The reverse: the cached values of the same tokens, as fp32 or bf16
+ * [T][heads][head_dim] (int8: fl(code * scale), then rounded for bf16; zeros
+ * for tokens without a page). */
+int kv_gather(const kv_cache *cache, int64_t layer, void *k, void *v, int x_dtype, int64_t T,
+              int64_t B, const int32_t *table, int64_t W, const int32_t *start,
+              const int32_t *cu, void *stream);
+
+/* Bytes of device workspace of kv_decode_attention (rows = B) and
+ * kv_prefill_attention (rows = T); 0 for invalid sizes. */
+size_t kv_attention_workspace_bytes(int64_t rows, int64_t B, int64_t q_heads, int64_t heads,
+                                    int64_t head_dim);
+
+/* Attention of one new token per sequence (already in the cache).
+ *   q, out  [B][q_heads][head_dim] of x_dtype, rows q_stride elements apart
+ *           (out contiguous); q_heads a multiple of the cache's heads, query
+ *           head h reads cache head h / (q_heads / heads).
+ *   lens    [B] cached tokens, the new one included: its position is
+ *           pos = lens[b] - 1.
+ *   window, sinks  token j is visible if j <= pos and (window == 0 or
+ *           j > pos - window or j < sinks).
+ *   out[b][h] = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * <q, k_j> - max),
+ *           over the visible tokens; zeros if there is none.  Products of
+ *           K and V with fp32 activations keep fp32 accuracy, sums are fp32.
+ *   workspace  kv_attention_workspace_bytes(B, B, q_heads, heads, head_dim)
+ *           bytes, 256-byte aligned; scratch.
+ * Results do not depend on the order in which workgroups run.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN,
+ * W4_ERR_WORKSPACE or W4_ERR_HIP. */
+int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,
+                        int64_t q_stride, int64_t B, int64_t q_heads, const int32_t *table,
+                        int64_t W, const int32_t *lens, float scale, int64_t window,
+                        int64_t sinks, void *out, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Attention of prompts or chunks of them: sequence b's queries are rows
+ * cu[b] .. cu[b + 1] - 1 of q (cu as in kv_append, required), the last tokens
+ * of its lens[b] cached ones: the query of row cu[b] + t has position
+ * pos = lens[b] - (cu[b + 1] - cu[b]) + t; one with a negative position sees
+ * nothing.  Everything else as kv_decode_attention; bf16 activations have the
+ * softmax weights rounded to bf16 before the product with V (their sum is
+ * taken after the rounding). */
+int kv_prefill_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,
+                         int64_t q_stride, int64_t T, int64_t B, int64_t q_heads,
+                         const int32_t *table, int64_t W, const int32_t *lens,
+                         const int32_t *cu, float scale, int64_t window, int64_t sinks,
+                         void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Copy whole pages, in every layer, from src to dst (the same cache or another
+ * of the same layers, heads, page_size, head_dim and dtype):
+ * page src_ids[i] of src to page dst_ids[i] of dst, 0 <= i < n (int32 device
+ * arrays; a pair with an id outside its cache is skipped).  A page must not be
+ * written twice nor written and read by one call. */
+int kv_copy_pages(const kv_cache *dst, const int32_t *dst_ids, const kv_cache *src,
+                  const int32_t *src_ids, int64_t n, void *stream);
+
+/* Give every slot the pages for add[s] more tokens.  A slot needs the pages of
+ * its row from the first -1 at or after entry lens[s] / page_size up to entry
+ * ceil((lens[s] + add[s]) / page_size) - 1.  Free pages (refs 0) are dealt in
+ * ascending order, to slots in ascending order, each page's refs set to 1; slot
+ * s is served (ok[s] = 1) if it needs none or the needs of slots 0 .. s
+ * together are not more than the free pages, else left as it was (ok[s] = 0).
+ * add[s] <= 0 needs nothing; a slot whose row is too short, or with a length outside
+ * [0, W * page_size], needs nothing and has ok 0.
+ *   workspace  8 * S + 256 bytes, 16-byte aligned. */
+int kv_reserve(int32_t *table, int64_t S, int64_t W, const int32_t *lens, int32_t *refs,
+               int64_t pages, int64_t page_size, const int32_t *add, int32_t *ok,
+               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Fork n sequences: slot children[i] becomes a copy of slot parents[i].  Full
+ * pages are shared (refs + 1); a last partial page is copied, in every layer,
+ * to a free page of the child's own, so that both can be appended to.  Free
+ * pages are dealt in ascending order to the forks that need one in order; fork
+ * i is granted (ok[i] = 1) if the needs of forks 0 .. i together are not more
+ * than the free pages.  Not granted: a slot outside [0, S), a child that is
+ * not empty (length 0 and first entry -1) or that an earlier i names too, a
+ * parent whose length is outside [0, W * page_size] or whose last partial page
+ * is none.  A child that is not granted stays empty.  Pages that a parent has
+ * reserved beyond its length stay its own.
+ *   workspace  16 * n + 256 bytes, 16-byte aligned. */
+int kv_fork(const kv_cache *cache, int32_t *table, int64_t S, int64_t W, int32_t *lens,
+            int32_t *refs, const int32_t *parents, const int32_t *children, int64_t n,
+            int32_t *ok, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Retire n slots: refs - 1 for every page of their rows, rows -1, lengths 0.
+ * Slots outside [0, S) are skipped, one named twice is retired once. */
+int kv_free(int32_t *table, int64_t S, int64_t W, int32_t *lens, int32_t *refs, int64_t pages,
+            const int32_t *slots, int64_t n, void *stream);
+
+/* Make the pool dense: with n = live[0] = the number of pages with refs > 0,
+ * the live pages at n and above move (every layer) into the free pages below
+ * n, i-th to i-th in ascending order, and the tables are renamed.
+ *   table_out [S][W], refs_out [pages]: may be table and refs (in place);
+ *   entries of the table that are no page come out as -1.
+ *   workspace  8 * pages + 256 bytes, 16-byte aligned. */
+int kv_compact(const kv_cache *cache, const int32_t *table, int64_t S, int64_t W,
+               const int32_t *refs, int32_t *table_out, int32_t *refs_out, int32_t *live,
+               void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *w4_status_string(int status);
 

@@ -27,7 +27,11 @@ functions carry the C names:
   -- the same tile layout for the W4A8 int4 codes and the forward on it;
 * ``awq_channel_scales``, ``awq_fold_weight``, ``awq_quantize_act``,
   ``awq_scale_act_bf16``, ``w4a8_linear_awq`` -- AWQ-style activation-aware
-  channel scaling (power-of-two scales from calibration activations).
+  channel scaling (power-of-two scales from calibration activations);
+* ``KVCache``, ``kv_append``, ``kv_gather``, ``kv_decode_attention``,
+  ``kv_prefill_attention``, ``kv_reserve``, ``kv_fork``, ``kv_free``,
+  ``kv_copy_pages``, ``kv_compact`` -- the paged key-value cache between the
+  quantized projections of a decoder layer (``kv.py``).
 
 There is no CPU fallback: without the built library (``build.py``) or
 without a GPU every call raises.
@@ -119,6 +123,7 @@ def lib():
             "w4_probe_mfma": ([_I, ctypes.c_int, _P, _P, _P, _P], ctypes.c_int),
             "w4_time_next_kernel": ([_P, _P], ctypes.c_int),
         }
+        sigs.update(SIGNATURES)
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -716,3 +721,9 @@ def w4a16_linear(X_bf16: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
                             _dev(Y, "Y", torch.float32, (M, N), dev), _stream(stream))
     _check("w4a16_linear", rc)
     return Y
+
+
+from .kv import (KV_BF16, KV_INT8, KV_X_BF16, KV_X_FP32, SIGNATURES, KVCache,  # noqa: E402
+                 kv_append, kv_attention_workspace_bytes, kv_compact, kv_copy_pages,
+                 kv_decode_attention, kv_fork, kv_free, kv_gather, kv_prefill_attention,
+                 kv_reserve)

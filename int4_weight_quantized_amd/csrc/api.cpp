@@ -9,6 +9,7 @@
 
 #include "../../include/w4.h"
 #include "kernels.h"
+#include "kv.h"
 
 // Device scratch of w4a8_linear_noalloc: the activation-code workspace of the
 // W4A8 paths, held in a fixed array so that the call allocates nothing.  In
@@ -181,6 +182,8 @@ int check_workspace(int64_t M, int64_t K, void *workspace, size_t bytes) {
 }  // namespace
 
 void w4::note_kernel(const void *kernel, hipStream_t) { g_pending_kernel = kernel; }
+
+int w4::finish_call(const char *path, hipError_t e) { return launched(path, e); }
 
 w4::TimingEvents w4::take_timing_events() {
     TimingEvents ev{g_time_start, g_time_stop};
