@@ -1,11 +1,13 @@
 // Attention over the paged key-value cache.
 #include <type_traits>
 
-#include "kv_common.h"
+#include "kv_attn.h"
 
 namespace w4 {
 
-size_t kv_attn_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 256; }
+size_t kv_attn_ws_bytes(int64_t, int64_t, int64_t hq, int64_t heads, int64_t D) {
+    return kv_decode_ws_bytes(hq, heads, D);
+}
 
 // One workgroup per query row and head: scores of 256 tokens at a time (one
 // token a thread), a running maximum and sum, and the weighted sum of V with
@@ -81,6 +83,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, hipStream_t st) {
+    if (!a.cu) return launch_kv_decode(a, st);
     const dim3 g((unsigned)a.T, (unsigned)a.hq);
     if (a.int8 && a.fp32)
         hipLaunchKernelGGL((k_kv_attn_rows<true, true>), g, dim3(256), 0, st, a);

@@ -1,0 +1,487 @@
+// Attention of one new token per sequence over the paged key-value cache.
+//
+//   s_j = scale <q, k_j>,  o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
+//
+// One pass over K and V with a running maximum m and sum.  Bound by memory:
+// every visible token's K and V are read once and meet G = q_heads / heads
+// query rows, 2 G flops a byte, so the matrix cores have time to spare.
+//
+// The rows are padded to the 16 columns of v_mfma_f32_16x16x32_bf16, and both
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T: the
+// accumulators of S^T (lane = query row, registers = tokens) are then the
+// B operand of the second product as they stand.  The order of the tokens
+// inside that product's depth of 32 is free, so lane group g takes tokens
+// 4g .. 4g+3 of both 16-token halves and P never leaves its lane.  Softmax
+// maxima and rescaling are one value a lane.
+//
+// K goes from memory to registers (16 rows of 64 bytes a load), V in whole
+// rows, transposed by byte permutes of register pairs; no LDS in the loop and
+// no barrier, waves of a workgroup take tiles of 32 tokens in turn and are
+// joined through LDS once per (sequence, cache head).
+//
+// fp32 activations: q and the softmax weights are split into three bf16 terms
+// (24 significant bits), each its own MFMA into the same fp32 accumulator; K
+// and V are exact in bf16 (int8 codes have 8 bits), so products keep fp32
+// accuracy.  bf16 activations: q is exact, the weights keep two terms (16
+// bits), so that the output's own rounding dominates.
+#include "kv_attn.h"
+
+namespace w4 {
+
+namespace {
+
+__device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// The tokens that a position sees, as tiles of 32: the first `sink_tiles`
+// tiles, then the tiles from lo / 32 to the end.
+struct Span {
+    int64_t n, lo;  // tokens 0 <= j < n with j >= lo or j < sinks
+    int64_t sink_tiles, lo_tile, tiles;
+};
+
+__device__ __forceinline__ Span make_span(const KvAttnArgs &a, int64_t len) {
+    Span s;
+    s.n = min(max(len, (int64_t)0), a.c.W << a.c.shift);
+    s.lo = a.window ? max(s.n - a.window, (int64_t)0) : 0;
+    s.lo_tile = s.lo / 32;
+    s.sink_tiles = min((a.sinks + 31) / 32, s.lo_tile);
+    s.tiles = s.sink_tiles + (s.n + 31) / 32 - s.lo_tile;
+    return s;
+}
+
+// One lane's VD consecutive values of a row.
+template <bool INT8, int VD>
+struct Piece {
+    static constexpr int kWords = VD * (INT8 ? 1 : 2) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const uint8_t *p) {
+        if constexpr (kWords == 1) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else if constexpr (kWords == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            w[0] = x.x, w[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+};
+
+// Value e of two pieces as a bf16 pair.
+template <bool INT8, int VD>
+__device__ __forceinline__ uint32_t pair(const Piece<INT8, VD> &x, const Piece<INT8, VD> &y,
+                                         int e) {
+    if constexpr (INT8)
+        return code_pair((int8_t)(x.w[e / 4] >> (e % 4 * 8)), (int8_t)(y.w[e / 4] >> (e % 4 * 8)));
+    else
+        return __builtin_amdgcn_perm(y.w[e / 2], x.w[e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// Query heads in groups of up to 16 that share a cache head: `per_head` groups
+// for each of the cache's heads, `rows` rows at most in one.
+struct KvHeads {
+    int group, rows, per_head, count;
+    __host__ __device__ explicit KvHeads(const KvAttnArgs &a) {
+        group = a.hq / a.c.heads;
+        rows = group < 16 ? group : 16;
+        per_head = (group + 15) / 16;
+        count = per_head * a.c.heads;
+    }
+};
+
+// Work of the split kernel.  A unit is one tile for each of NW waves of one
+// (sequence, head) pair; pairs follow one another, sequence-major, and the U
+// units of all pairs are dealt to the first n = min(workgroups, U) workgroups in
+// equal runs: workgroup k has units floor(k U / n) to floor((k + 1) U / n),
+// whatever the lengths are.  A sequence without tokens has one unit (its outputs are zeros).
+struct KvCursor {
+    int64_t b;  // the pair
+    int h;
+    int64_t u, left;  // first unit of the pair, units left of the run
+};
+
+template <int NW>
+__device__ __forceinline__ int64_t pair_units(const KvAttnArgs &a, int64_t b) {
+    return max((make_span(a, a.lens[b]).tiles + NW - 1) / NW, (int64_t)1);
+}
+
+// Units of a pair of sequence b0 + lane, and their running sum over the lanes.
+template <int NW>
+__device__ __forceinline__ int64_t scan_units(const KvAttnArgs &a, int64_t b0, int64_t &units) {
+    const int lane = threadIdx.x % kWave;
+    units = b0 + lane < a.B ? pair_units<NW>(a, b0 + lane) : 0;
+    int64_t s = units;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int64_t t = __shfl_up(s, o, kWave);
+        if (lane >= o) s += t;
+    }
+    return s;
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Units of all pairs (wave-uniform).
+template <int NW>
+__device__ __forceinline__ int64_t all_units(const KvAttnArgs &a, const KvHeads &hd) {
+    int64_t sum = 0, units;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kWave)
+        sum += __shfl(scan_units<NW>(a, b0, units), kWave - 1, kWave);
+    return uniform(sum) * hd.count;
+}
+
+template <int NW>
+__device__ __forceinline__ KvCursor kv_first_segment(const KvAttnArgs &a, const KvHeads &hd,
+                                                     int64_t k, int64_t n) {
+    const int64_t U = all_units<NW>(a, hd);
+    n = min(n, U);
+    if (k >= n) return KvCursor{0, 0, 0, 0};
+    const int64_t first = k * U / n, last = (k + 1) * U / n;
+    KvCursor cur{0, 0, 0, last - first};
+    int64_t before = 0, units;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kWave) {
+        const int64_t s = scan_units<NW>(a, b0, units);
+        // the first sequence whose units end behind `first`
+        const uint64_t hit = __ballot((before + s) * hd.count > first);
+        if (hit) {
+            const int at = __ffsll((unsigned long long)hit) - 1;
+            const int64_t un = uniform(__shfl(units, at, kWave));
+            const int64_t off = first - (before + uniform(__shfl(s, at, kWave)) - un) * hd.count;
+            cur.b = b0 + at;
+            cur.h = (int)(off / un);
+            cur.u = off - cur.h * un;
+            return cur;
+        }
+        before += uniform(__shfl(s, kWave - 1, kWave));
+    }
+    cur.left = 0;  // (not reached: first < U)
+    return cur;
+}
+
+// The first and last workgroup of n that have units of pair (b, h).
+template <int NW>
+__device__ __forceinline__ void kv_blocks_of(const KvAttnArgs &a, const KvHeads &hd, int64_t b,
+                                             int h, int64_t n, int64_t &k0, int64_t &k1) {
+    int64_t U = 0, first = 0, un = 1, units;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kWave) {
+        const int64_t s = scan_units<NW>(a, b0, units);
+        if (b >= b0 && b < b0 + kWave) {
+            un = uniform(__shfl(units, (int)(b - b0), kWave));
+            first = (U + uniform(__shfl(s, (int)(b - b0), kWave)) - un) * hd.count + h * un;
+        }
+        U += uniform(__shfl(s, kWave - 1, kWave));
+    }
+    U *= hd.count;
+    n = min(n, U);
+    k0 = ((first + 1) * n - 1) / U;
+    k1 = ((first + un) * n - 1) / U;
+}
+
+// The part of a pair that a workgroup leaves in the workspace: unnormalized
+// sums, maxima and sums of weights.  Slot 2 k + 1: workgroup k's part that
+// starts a pair, slot 2 k: one that does not.
+struct KvPartial {
+    float *o, *m, *l;
+    __device__ KvPartial(const KvAttnArgs &a, const KvHeads &hd, int DP, int64_t slot) {
+        o = reinterpret_cast<float *>(a.ws) + slot * hd.rows * (DP + 2);
+        m = o + hd.rows * DP;
+        l = m + hd.rows;
+    }
+};
+
+}  // namespace
+
+// DP: head_dim rounded up to 64, 128 or 256 (values beyond head_dim: q is zero
+// there, and their V rows are not stored).  NW: waves.  SPLIT: the workgroups
+// share all units of work evenly (see unit_range), else workgroup i has all of
+// (sequence, head) i.
+template <int DP, bool INT8, bool FP32, int NW, bool SPLIT>
+__global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
+    constexpr int kSteps = DP / 32, VD = DP / 16;
+    constexpr int kQ = FP32 ? 3 : 1, kP = FP32 ? 3 : 2;
+    constexpr int kRow = DP + 4;  // LDS row of the join, padded off the banks
+    extern __shared__ float lds[];
+    const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const KvHeads hd(a);
+    float *sm = lds + NW * hd.rows * kRow, *sl = sm + NW * 16;
+    const float scale2 = a.scale * 1.44269504088896340736f;
+    const int D = a.c.D;
+
+    KvCursor cur = SPLIT ? kv_first_segment<NW>(a, hd, blockIdx.x, gridDim.x)
+                         : KvCursor{(int64_t)blockIdx.x / hd.count, (int)(blockIdx.x % hd.count),
+                                    0, (int64_t)1 << 40};
+    while (cur.left > 0) {
+        const int64_t b = cur.b;
+        const Span sp = make_span(a, a.lens[b]);
+        const int64_t units = max((sp.tiles + NW - 1) / NW, (int64_t)1);
+        const int64_t u0 = cur.u, u1 = min(units, u0 + cur.left);
+        const int kvh = cur.h / hd.per_head, part = cur.h % hd.per_head;
+        const int rows = min(hd.group - part * 16, 16);
+        const int64_t qrow = b * a.ldq + ((int64_t)kvh * hd.group + part * 16) * D;
+
+        // q as the B operand: lane c holds row c, group g its share of each 32 dims
+        uint4 q[kQ][kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = INT8 ? s / 2 * 64 + g * 16 + s % 2 * 8 : s * 32 + g * 8;
+            load_query<FP32>(a.q, qrow + (int64_t)c * D + d, c < rows && d < D, q, s);
+        }
+        v4f o[VD] = {};
+        float m = -INFINITY, l = 0.0f;
+        const int32_t *table = a.c.table + b * a.c.W;
+        const int64_t last = min(u1 * NW, sp.tiles);
+        for (int64_t i = u0 * NW + wave; i < last; i += NW) {
+            const int64_t t0 = 32 * (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.lo_tile);
+            const int p0 = kv_page(a.c, table, t0), p1 = kv_page(a.c, table, t0 + 16);
+            const int64_t v0 = kv_vector(a.c, max(p0, 0), kvh, t0);
+            const int64_t v1 = kv_vector(a.c, max(p1, 0), kvh, t0 + 16);
+            constexpr int kB = INT8 ? 1 : 2;
+            uint4 k[2][INT8 ? kSteps / 2 : kSteps];
+            Piece<INT8, VD> v[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *kp = a.c.k + ((h ? v1 : v0) + c) * D * kB;
+#pragma unroll
+                for (int s = 0; s < (INT8 ? kSteps / 2 : kSteps); ++s) {
+                    const int d = INT8 ? s * 64 + g * 16 : s * 32 + g * 8;
+                    k[h][s] = *reinterpret_cast<const uint4 *>(kp + (d < D ? d : 0) * kB);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *vp = a.c.v + ((h ? v1 : v0) + g * 4) * D * kB +
+                                    (c * VD < D ? c * VD : 0) * kB;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[h][j].load(vp + j * D * kB);
+            }
+            float ks[2][4], vs[2][4];
+            if constexpr (INT8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t at = (h ? v1 : v0) + g * 4;
+                    const float4 x = *reinterpret_cast<const float4 *>(a.c.ks + at);
+                    const float4 y = *reinterpret_cast<const float4 *>(a.c.vs + at);
+                    ks[h][0] = x.x, ks[h][1] = x.y, ks[h][2] = x.z, ks[h][3] = x.w;
+                    vs[h][0] = y.x, vs[h][1] = y.y, vs[h][2] = y.z, vs[h][3] = y.w;
+                }
+            }
+
+            float x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v4f s4 = {};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const uint4 kk = INT8 ? codes8(k[h][s / (INT8 ? 2 : 1)], s % 2) : k[h][s];
+#pragma unroll
+                    for (int t = kQ - 1; t >= 0; --t) s4 = mfma16(kk, q[t][s], s4);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[h][r] = s4[r] * (INT8 ? scale2 * ks[h][r] : scale2);
+            }
+            // tiles at an edge, or with a page missing: hide tokens, and clear
+            // their V, which may hold anything (0 * NaN would stay)
+            if (t0 + 32 > sp.n || (t0 < sp.lo && t0 + 32 > a.sinks) || p0 < 0 || p1 < 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int64_t t = t0 + 16 * h + 4 * g + r;
+                        const bool see = t < sp.n && (t >= sp.lo || t < a.sinks) &&
+                                         (h ? p1 : p0) >= 0;
+                        if (!see) {
+                            x[h][r] = -INFINITY;
+                            v[h][r].zero();
+                            if constexpr (INT8) vs[h][r] = 0.0f;
+                        }
+                    }
+            }
+            float mt = x[0][0];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mt = fmaxf(mt, x[h][r]);
+            mt = fmaxf(mt, __shfl_xor(mt, 16, kWave));
+            mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
+            if (__any(mt > m)) {
+                const float mn = fmaxf(m, mt);
+                const float alpha = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= alpha;
+#pragma unroll
+                for (int e = 0; e < VD; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[e][r] *= alpha;
+            }
+            const float mu = m == -INFINITY ? 0.0f : m;
+            float p[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = __builtin_amdgcn_exp2f(x[h][r] - mu);
+                    l += e;
+                    p[4 * h + r] = INT8 ? e * vs[h][r] : e;
+                }
+            uint4 pb[kP];
+            split_bf16<kP>(p, pb);
+#pragma unroll
+            for (int e = 0; e < VD; ++e) {
+                const uint4 vt = {pair(v[0][0], v[0][1], e), pair(v[0][2], v[0][3], e),
+                                  pair(v[1][0], v[1][1], e), pair(v[1][2], v[1][3], e)};
+#pragma unroll
+                for (int t = kP - 1; t >= 0; --t) o[e] = mfma16(vt, pb[t], o[e]);
+            }
+        }
+
+        // join the waves: a common maximum, then the sum of the rescaled parts
+        l += __shfl_xor(l, 16, kWave);
+        l += __shfl_xor(l, 32, kWave);
+        if (g == 0) sm[wave * 16 + c] = m, sl[wave * 16 + c] = l;
+        __syncthreads();
+        float mx = sm[c];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) mx = fmaxf(mx, sm[w * 16 + c]);
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
+        if (c < rows) {
+            float *to = lds + (wave * hd.rows + c) * kRow + g * 4 * VD;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < VD; e += 4)
+                    *reinterpret_cast<float4 *>(to + r * VD + e) =
+                        float4{o[e][r] * f, o[e + 1][r] * f, o[e + 2][r] * f, o[e + 3][r] * f};
+        }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == units;
+        const KvPartial part_ws(a, hd, DP, (int64_t)blockIdx.x * 2 + (u0 == 0));
+        for (int at = threadIdx.x; at < rows * (DP / 4); at += NW * 64) {
+            const int r = at / (DP / 4), d = at % (DP / 4) * 4;
+            float mr = sm[r];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) mr = fmaxf(mr, sm[w * 16 + r]);
+            float lr = 0.0f;
+            float4 y = {};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float mw = sm[w * 16 + r];
+                lr += mw == -INFINITY ? 0.0f : sl[w * 16 + r] * __builtin_amdgcn_exp2f(mw - mr);
+                const float4 z =
+                    *reinterpret_cast<const float4 *>(lds + (w * hd.rows + r) * kRow + d);
+                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            if (SPLIT && !whole) {
+                *reinterpret_cast<float4 *>(part_ws.o + r * DP + d) = y;
+                if (d == 0) part_ws.m[r] = mr, part_ws.l[r] = lr;
+            } else if (d < D) {
+                store_out<FP32>(a.out, (b * a.hq + (int64_t)kvh * hd.group + part * 16 + r) * D + d,
+                                y, lr);
+            }
+        }
+        __syncthreads();
+        if (!SPLIT) break;
+        cur.left -= u1 - u0;
+        cur.u = 0;
+        if (++cur.h == hd.count) cur.h = 0, ++cur.b;
+    }
+}
+
+// Joins the parts of the (sequence, head) pairs whose units went to more than
+// one workgroup, in the workgroups' order.
+template <int DP, bool FP32, int NW>
+__global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a, int blocks) {
+    const KvHeads hd(a);
+    const int64_t b = blockIdx.x / hd.count;
+    const int h = (int)(blockIdx.x % hd.count);
+    int64_t k0, k1;
+    kv_blocks_of<NW>(a, hd, b, h, blocks, k0, k1);
+    if (k0 == k1) return;
+    const int kvh = h / hd.per_head, part = h % hd.per_head, D = a.c.D;
+    const int rows = min(hd.group - part * 16, 16);
+    for (int at = threadIdx.x; at < rows * (DP / 4); at += 256) {
+        const int r = at / (DP / 4), d = at % (DP / 4) * 4;
+        float m = -INFINITY, l = 0.0f;
+        float4 y = {};
+        for (int64_t k = k0; k <= k1; ++k) {
+            const KvPartial p(a, hd, DP, k * 2 + (k == k0));
+            const float mk = p.m[r];
+            const float4 z = *reinterpret_cast<const float4 *>(p.o + r * DP + d);
+            if (mk == -INFINITY) continue;
+            const float mn = fmaxf(m, mk);
+            const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+            const float fb = __builtin_amdgcn_exp2f(mk - mn);
+            m = mn;
+            l = l * fa + p.l[r] * fb;
+            y.x = y.x * fa + z.x * fb;
+            y.y = y.y * fa + z.y * fb;
+            y.z = y.z * fa + z.z * fb;
+            y.w = y.w * fa + z.w * fb;
+        }
+        if (d < D)
+            store_out<FP32>(a.out, (b * a.hq + (int64_t)kvh * hd.group + part * 16 + r) * D + d, y,
+                            l);
+    }
+}
+
+namespace {
+
+constexpr int kSplitWaves = 4, kWholeWaves = 8, kSplitBlocks = 1024;
+constexpr int64_t kWholeTokens = 2048;
+
+template <int DP, bool INT8, bool FP32>
+hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
+    const KvHeads hd(a);
+    const int64_t pairs = a.B * hd.count;
+    // Tokens of the longest sequence that the table can hold and the window shows
+    int64_t most = a.c.W << a.c.shift;
+    if (a.window) most = std::min(most, a.window + a.sinks + 64);
+    if (most <= kWholeTokens) {
+        const size_t lds = (size_t)kWholeWaves * (hd.rows * (DP + 4) + 32) * 4;
+        auto *k = k_kv_decode<DP, INT8, FP32, kWholeWaves, false>;
+        hipLaunchKernelGGL(k, dim3((unsigned)pairs), dim3(kWholeWaves * 64), lds, st, a);
+    } else {
+        const size_t lds = (size_t)kSplitWaves * (hd.rows * (DP + 4) + 32) * 4;
+        auto *k = k_kv_decode<DP, INT8, FP32, kSplitWaves, true>;
+        hipLaunchKernelGGL(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
+        hipLaunchKernelGGL((k_kv_decode_join<DP, FP32, kSplitWaves>), dim3((unsigned)pairs),
+                           dim3(256), 0, st, a, (int)kSplitBlocks);
+    }
+    return hipGetLastError();
+}
+
+template <int DP>
+hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
+    if (a.int8) return a.fp32 ? launch_dp<DP, true, true>(a, st) : launch_dp<DP, true, false>(a, st);
+    return a.fp32 ? launch_dp<DP, false, true>(a, st) : launch_dp<DP, false, false>(a, st);
+}
+
+}  // namespace
+
+size_t kv_decode_ws_bytes(int64_t hq, int64_t heads, int64_t D) {
+    const int64_t rows = std::min<int64_t>(hq / heads, 16);
+    const int64_t DP = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    return (size_t)(kSplitBlocks * 2 * rows * (DP + 2) * 4);
+}
+
+hipError_t launch_kv_decode(const KvAttnArgs &a, hipStream_t st) {
+    return a.c.D <= 64 ? launch_types<64>(a, st)
+           : a.c.D <= 128 ? launch_types<128>(a, st)
+                          : launch_types<256>(a, st);
+}
+
+}  // namespace w4
