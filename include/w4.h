@@ -385,7 +385,8 @@ int w4a8_linear_prepacked(const float *X, int64_t M, int64_t K, int64_t N,
  * Values in device memory cannot be checked on the host; the kernels read and
  * write nothing outside the arrays whatever the tables, lengths and offsets
  * hold: a table entry outside [0, pages) is no page, a token without a page is
- * neither written nor attended, lengths are limited to [0, W * page_size].
+ * neither written nor attended, lengths are limited to W * page_size and 2^30
+ * (below 0: 0).
  * Slots of pages that hold no token yet may hold anything (NaN included). */
 typedef enum { KV_BF16 = 0, KV_INT8 = 1 } kv_dtype;
 
@@ -451,9 +452,8 @@ int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int
  * cu[b] .. cu[b + 1] - 1 of q (cu as in kv_append, required), the last tokens
  * of its lens[b] cached ones: the query of row cu[b] + t has position
  * pos = lens[b] - (cu[b + 1] - cu[b]) + t; one with a negative position sees
- * nothing.  Everything else as kv_decode_attention; bf16 activations have the
- * softmax weights rounded to bf16 before the product with V (their sum is
- * taken after the rounding). */
+ * nothing.  Everything else as kv_decode_attention; with bf16 activations the
+ * softmax weights are rounded to bf16 for the product with V. */
 int kv_prefill_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,
                          int64_t q_stride, int64_t T, int64_t B, int64_t q_heads,
                          const int32_t *table, int64_t W, const int32_t *lens,

@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libw4.so")
 ARCH = "gfx950"
 
 SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "w4a16.hip", "generic.hip", "probe.hip", "kv_cache.hip",
-           "kv_attn.hip", "kv_decode.hip", "kv_api.cpp", "api.cpp"]
+           "kv_attn.hip", "kv_decode.hip", "kv_prefill.hip",
+           "kv_api.cpp", "api.cpp"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -45,7 +45,7 @@ struct KvAttnArgs {
     int64_t T, B;
     int hq;              // query heads
     float scale;
-    int64_t window, sinks;
+    int window, sinks;   // at most 2^30
     void *ws;
 };
 

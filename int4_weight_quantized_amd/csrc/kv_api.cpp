@@ -2,6 +2,7 @@
 // anything is launched) and the calls of the launchers.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -17,6 +18,7 @@ constexpr int64_t kMaxValues = (int64_t)1 << 46;  // values of K in a cache
 // a grid dimension holds fewer than 2^32 threads: rows of a call (256 threads
 // each at most) and token-head vectors (32 threads each at most)
 constexpr int64_t kMaxRows = (int64_t)1 << 23;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // of one sequence
 constexpr int64_t kMaxVectors = (int64_t)1 << 26;
 
 // a * b, or kMaxValues + 1 where it is more (a, b >= 1)
@@ -145,8 +147,8 @@ int attention(const char *path, const kv_cache *c, int64_t layer, const void *q,
     a.B = B;
     a.hq = (int)hq;
     a.scale = scale;
-    a.window = window;
-    a.sinks = sinks;
+    a.window = (int)std::min(window, kMaxTokens);
+    a.sinks = (int)std::min(sinks, kMaxTokens);
     a.ws = workspace;
     return w4::finish_call(path, w4::launch_kv_attention(a, hip_stream(stream)));
 }

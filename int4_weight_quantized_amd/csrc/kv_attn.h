@@ -84,6 +84,12 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, float4 y, float
             uint2{pack_bf16(y.x, y.y), pack_bf16(y.z, y.w)};
 }
 
+// Length of sequence b: positions are 32-bit.
+constexpr int64_t kMaxLength = (int64_t)1 << 30;
+__device__ __forceinline__ int kv_length(const KvAttnArgs &a, int64_t b) {
+    return min(max(a.lens[b], 0), (int)min(a.c.W << a.c.shift, kMaxLength));
+}
+
 // First vector (page, head, slot) of the 16 tokens from `token` on.
 __device__ __forceinline__ int64_t kv_vector(const KvView &c, int page, int head, int64_t token) {
     return (((int64_t)page * c.heads + head) << c.shift) + (token & ((1 << c.shift) - 1));

@@ -38,14 +38,14 @@ __device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
 // The tokens that a position sees, as tiles of 32: the first `sink_tiles`
 // tiles, then the tiles from lo / 32 to the end.
 struct Span {
-    int64_t n, lo;  // tokens 0 <= j < n with j >= lo or j < sinks
-    int64_t sink_tiles, lo_tile, tiles;
+    int n, lo;  // tokens 0 <= j < n with j >= lo or j < sinks
+    int sink_tiles, lo_tile, tiles;
 };
 
-__device__ __forceinline__ Span make_span(const KvAttnArgs &a, int64_t len) {
+__device__ __forceinline__ Span make_span(const KvAttnArgs &a, int64_t b) {
     Span s;
-    s.n = min(max(len, (int64_t)0), a.c.W << a.c.shift);
-    s.lo = a.window ? max(s.n - a.window, (int64_t)0) : 0;
+    s.n = kv_length(a, b);
+    s.lo = a.window ? max(s.n - a.window, 0) : 0;
     s.lo_tile = s.lo / 32;
     s.sink_tiles = min((a.sinks + 31) / 32, s.lo_tile);
     s.tiles = s.sink_tiles + (s.n + 31) / 32 - s.lo_tile;
@@ -106,13 +106,13 @@ struct KvHeads {
 // whatever the lengths are.  A sequence without tokens has one unit (its outputs are zeros).
 struct KvCursor {
     int64_t b;  // the pair
-    int h;
-    int64_t u, left;  // first unit of the pair, units left of the run
+    int h, u;      // the head, the first unit of the pair
+    int64_t left;  // units left of the run
 };
 
 template <int NW>
 __device__ __forceinline__ int64_t pair_units(const KvAttnArgs &a, int64_t b) {
-    return max((make_span(a, a.lens[b]).tiles + NW - 1) / NW, (int64_t)1);
+    return max((make_span(a, b).tiles + NW - 1) / NW, 1);
 }
 
 // Units of a pair of sequence b0 + lane, and their running sum over the lanes.
@@ -163,7 +163,7 @@ __device__ __forceinline__ KvCursor kv_first_segment(const KvAttnArgs &a, const 
             const int64_t off = first - (before + uniform(__shfl(s, at, kWave)) - un) * hd.count;
             cur.b = b0 + at;
             cur.h = (int)(off / un);
-            cur.u = off - cur.h * un;
+            cur.u = (int)(off - cur.h * un);
             return cur;
         }
         before += uniform(__shfl(s, kWave - 1, kWave));
@@ -227,9 +227,9 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
                                     0, (int64_t)1 << 40};
     while (cur.left > 0) {
         const int64_t b = cur.b;
-        const Span sp = make_span(a, a.lens[b]);
-        const int64_t units = max((sp.tiles + NW - 1) / NW, (int64_t)1);
-        const int64_t u0 = cur.u, u1 = min(units, u0 + cur.left);
+        const Span sp = make_span(a, b);
+        const int units = max((sp.tiles + NW - 1) / NW, 1);
+        const int u0 = cur.u, u1 = (int)min((int64_t)units, u0 + cur.left);
         const int kvh = cur.h / hd.per_head, part = cur.h % hd.per_head;
         const int rows = min(hd.group - part * 16, 16);
         const int64_t qrow = b * a.ldq + ((int64_t)kvh * hd.group + part * 16) * D;
@@ -244,9 +244,9 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
         v4f o[VD] = {};
         float m = -INFINITY, l = 0.0f;
         const int32_t *table = a.c.table + b * a.c.W;
-        const int64_t last = min(u1 * NW, sp.tiles);
-        for (int64_t i = u0 * NW + wave; i < last; i += NW) {
-            const int64_t t0 = 32 * (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.lo_tile);
+        const int last = min(u1 * NW, sp.tiles);
+        for (int i = u0 * NW + wave; i < last; i += NW) {
+            const int t0 = 32 * (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.lo_tile);
             const int p0 = kv_page(a.c, table, t0), p1 = kv_page(a.c, table, t0 + 16);
             const int64_t v0 = kv_vector(a.c, max(p0, 0), kvh, t0);
             const int64_t v1 = kv_vector(a.c, max(p1, 0), kvh, t0 + 16);
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int64_t t = t0 + 16 * h + 4 * g + r;
+                        const int t = t0 + 16 * h + 4 * g + r;
                         const bool see = t < sp.n && (t >= sp.lo || t < a.sinks) &&
                                          (h ? p1 : p0) >= 0;
                         if (!see) {
@@ -449,7 +449,7 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     const int64_t pairs = a.B * hd.count;
     // Tokens of the longest sequence that the table can hold and the window shows
     int64_t most = a.c.W << a.c.shift;
-    if (a.window) most = std::min(most, a.window + a.sinks + 64);
+    if (a.window) most = std::min<int64_t>(most, (int64_t)a.window + a.sinks + 64);
     if (most <= kWholeTokens) {
         const size_t lds = (size_t)kWholeWaves * (hd.rows * (DP + 4) + 32) * 4;
         auto *k = k_kv_decode<DP, INT8, FP32, kWholeWaves, false>;
