@@ -14,10 +14,12 @@
 // 4g .. 4g+3 of both 16-token halves and P never leaves its lane.  Softmax
 // maxima and rescaling are one value a lane.
 //
-// K goes from memory to registers (16 rows of 64 bytes a load), V in whole
-// rows, transposed by byte permutes of register pairs; no LDS in the loop and
-// no barrier, waves of a workgroup take tiles of 32 tokens in turn and are
-// joined through LDS once per (sequence, cache head).
+// K and V are read in whole rows with non-temporal loads (each byte is used
+// once; half rows, as the A operand wants K, made every line two requests).  K
+// goes through 16 rows of the wave's own LDS into the A operand, V is transposed
+// by byte permutes of register pairs.  No barrier in the loop: the waves of a
+// workgroup take tiles of 32 tokens in turn and are joined through LDS once per
+// (sequence, cache head).
 //
 // fp32 activations: q and the softmax weights are split into three bf16 terms
 // (24 significant bits), each its own MFMA into the same fp32 accumulator; K
@@ -28,6 +30,10 @@
 
 namespace w4 {
 
+#ifndef KV_WAVES
+#define KV_WAVES (DP == 256 ? (FP32 ? 1 : 2) : DP == 128 && FP32 && !INT8 ? 2 : 3)
+#define KV_BLOCKS 768
+#endif
 namespace {
 
 __device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
@@ -52,6 +58,8 @@ __device__ __forceinline__ Span make_span(const KvAttnArgs &a, int64_t b) {
     return s;
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // One lane's VD consecutive values of a row.
 template <bool INT8, int VD>
 struct Piece {
@@ -59,15 +67,16 @@ struct Piece {
     uint32_t w[kWords];
     __device__ __forceinline__ void load(const uint8_t *p) {
         if constexpr (kWords == 1) {
-            w[0] = *reinterpret_cast<const uint32_t *>(p);
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));
         } else if constexpr (kWords == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = x.x, w[1] = x.y;
+            const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+            w[0] = x[0], w[1] = x[1];
         } else {
 #pragma unroll
             for (int i = 0; i < kWords; i += 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
-                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+                const u32x4 x =
+                    __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + 4 * i));
+                w[i] = x[0], w[i + 1] = x[1], w[i + 2] = x[2], w[i + 3] = x[3];
             }
         }
     }
@@ -85,6 +94,22 @@ __device__ __forceinline__ uint32_t pair(const Piece<INT8, VD> &x, const Piece<I
         return code_pair((int8_t)(x.w[e / 4] >> (e % 4 * 8)), (int8_t)(y.w[e / 4] >> (e % 4 * 8)));
     else
         return __builtin_amdgcn_perm(y.w[e / 2], x.w[e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// A wave's 32 tokens.
+template <int DP, bool INT8>
+struct Tile {
+    u32x4 k[2][INT8 ? DP / 64 : DP / 32];
+    Piece<INT8, DP / 16> v[2][4];
+    v4f ks[2], vs[2];
+    int t0, page[2];
+};
+
+// Byte offset of 16-byte chunk `ch` of row `row` among 16 rows of kCh chunks,
+// XOR-swizzled so that 16 rows' chunks of one index cover all banks once.
+template <int kCh>
+__device__ __forceinline__ int stage_at(int row, int ch) {
+    return row * kCh * 16 + ((ch ^ (kCh == 8 ? row >> 1 & 7 : row & 15)) << 4);
 }
 
 // Query heads in groups of up to 16 that share a cache head: `per_head` groups
@@ -210,15 +235,21 @@ struct KvPartial {
 // share all units of work evenly (see unit_range), else workgroup i has all of
 // (sequence, head) i.
 template <int DP, bool INT8, bool FP32, int NW, bool SPLIT>
-__global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
-    constexpr int kSteps = DP / 32, VD = DP / 16;
+__global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
+    constexpr int kSteps = DP / 32, VD = DP / 16, kB = INT8 ? 1 : 2;
+    constexpr int kLoads = INT8 ? kSteps / 2 : kSteps;
+    constexpr int kCh = DP * kB / 16, kRowsPer = 64 / kCh;  // 16-byte chunks of a row, rows of a load
     constexpr int kQ = FP32 ? 3 : 1, kP = FP32 ? 3 : 2;
     constexpr int kRow = DP + 4;  // LDS row of the join, padded off the banks
     extern __shared__ float lds[];
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const KvHeads hd(a);
-    float *sm = lds + NW * hd.rows * kRow, *sl = sm + NW * 16;
+    // LDS: maxima and sums of the join, then its rows, in the same place as the
+    // waves' K tiles of the loop (a barrier lies between)
+    float *sm = lds, *sl = sm + NW * 16;
+    float *join = sl + NW * 16;
+    uint8_t *stage = reinterpret_cast<uint8_t *>(join) + wave * 16 * DP * kB;
     const float scale2 = a.scale * 1.44269504088896340736f;
     const int D = a.c.D;
 
@@ -245,69 +276,91 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
         float m = -INFINITY, l = 0.0f;
         const int32_t *table = a.c.table + b * a.c.W;
         const int last = min(u1 * NW, sp.tiles);
-        for (int i = u0 * NW + wave; i < last; i += NW) {
-            const int t0 = 32 * (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.lo_tile);
-            const int p0 = kv_page(a.c, table, t0), p1 = kv_page(a.c, table, t0 + 16);
-            const int64_t v0 = kv_vector(a.c, max(p0, 0), kvh, t0);
-            const int64_t v1 = kv_vector(a.c, max(p1, 0), kvh, t0 + 16);
-            constexpr int kB = INT8 ? 1 : 2;
-            uint4 k[2][INT8 ? kSteps / 2 : kSteps];
-            Piece<INT8, VD> v[2][4];
+        auto tile_token = [&](int i) {
+            return 32 * (i < sp.sink_tiles ? i : i - sp.sink_tiles + sp.lo_tile);
+        };
+        // pages of this wave's next 32 tiles, one lane for each 16 tokens: one
+        // load for all of them, off the path of the loads that need them
+        int base = 0, pages = -1;
+        auto look_up = [&](int i) {
+            const int ii = i + lane / 2 * NW;
+            base = i;
+            pages = ii < last ? kv_page(a.c, table, tile_token(ii) + lane % 2 * 16) : -1;
+        };
+        auto load = [&](Tile<DP, INT8> &t, int i) {
+            if (i - base >= 32 * NW) look_up(i);
+            const int at = (i - base) / NW * 2;
+            t.t0 = tile_token(i);
+            t.page[0] = __builtin_amdgcn_readlane(pages, at);
+            t.page[1] = __builtin_amdgcn_readlane(pages, at + 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint8_t *kp = a.c.k + ((h ? v1 : v0) + c) * D * kB;
+                const int64_t vec = kv_vector(a.c, max(t.page[h], 0), kvh, t.t0 + 16 * h);
 #pragma unroll
-                for (int s = 0; s < (INT8 ? kSteps / 2 : kSteps); ++s) {
-                    const int d = INT8 ? s * 64 + g * 16 : s * 32 + g * 8;
-                    k[h][s] = *reinterpret_cast<const uint4 *>(kp + (d < D ? d : 0) * kB);
+                for (int s = 0; s < kLoads; ++s) {
+                    // whole rows one after another (rows of 64 bytes: one load
+                    // has all 16, each lane its own place of the A operand)
+                    const int row = kCh > 4 ? s * kRowsPer + lane / kCh : c;
+                    const int d = (kCh > 4 ? lane % kCh : g) * (16 / kB);
+                    t.k[h][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(
+                        a.c.k + ((vec + row) * D + (d < D ? d : 0)) * kB));
                 }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint8_t *vp = a.c.v + ((h ? v1 : v0) + g * 4) * D * kB +
-                                    (c * VD < D ? c * VD : 0) * kB;
+                const int64_t vec = kv_vector(a.c, max(t.page[h], 0), kvh, t.t0 + 16 * h) + g * 4;
+                const uint8_t *vp = a.c.v + vec * D * kB + (c * VD < D ? c * VD : 0) * kB;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[h][j].load(vp + j * D * kB);
-            }
-            float ks[2][4], vs[2][4];
-            if constexpr (INT8) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t at = (h ? v1 : v0) + g * 4;
-                    const float4 x = *reinterpret_cast<const float4 *>(a.c.ks + at);
-                    const float4 y = *reinterpret_cast<const float4 *>(a.c.vs + at);
-                    ks[h][0] = x.x, ks[h][1] = x.y, ks[h][2] = x.z, ks[h][3] = x.w;
-                    vs[h][0] = y.x, vs[h][1] = y.y, vs[h][2] = y.z, vs[h][3] = y.w;
+                for (int j = 0; j < 4; ++j) t.v[h][j].load(vp + j * D * kB);
+                if constexpr (INT8) {
+                    t.ks[h] = *reinterpret_cast<const v4f *>(a.c.ks + vec);
+                    t.vs[h] = *reinterpret_cast<const v4f *>(a.c.vs + vec);
                 }
             }
-
+        };
+        auto compute = [&](Tile<DP, INT8> &t) {
             float x[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                // rows -> the A operand (lane: row c, chunk 4 s + g) through this
+                // wave's LDS; a wave's LDS operations are in order
+                if constexpr (kCh > 4) {
+#pragma unroll
+                    for (int s = 0; s < kLoads; ++s)
+                        *reinterpret_cast<u32x4 *>(
+                            stage + stage_at<kCh>(s * kRowsPer + lane / kCh, lane % kCh)) = t.k[h][s];
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int s = 0; s < kLoads; ++s)
+                        t.k[h][s] =
+                            *reinterpret_cast<const u32x4 *>(stage + stage_at<kCh>(c, 4 * s + g));
+                    __builtin_amdgcn_wave_barrier();
+                }
                 v4f s4 = {};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const uint4 kk = INT8 ? codes8(k[h][s / (INT8 ? 2 : 1)], s % 2) : k[h][s];
+                    const uint4 raw = __builtin_bit_cast(uint4, t.k[h][INT8 ? s / 2 : s]);
+                    const uint4 kk = INT8 ? codes8(raw, s % 2) : raw;
 #pragma unroll
-                    for (int t = kQ - 1; t >= 0; --t) s4 = mfma16(kk, q[t][s], s4);
+                    for (int u = kQ - 1; u >= 0; --u) s4 = mfma16(kk, q[u][s], s4);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[h][r] = s4[r] * (INT8 ? scale2 * ks[h][r] : scale2);
+                for (int r = 0; r < 4; ++r) x[h][r] = s4[r] * (INT8 ? scale2 * t.ks[h][r] : scale2);
             }
             // tiles at an edge, or with a page missing: hide tokens, and clear
             // their V, which may hold anything (0 * NaN would stay)
-            if (t0 + 32 > sp.n || (t0 < sp.lo && t0 + 32 > a.sinks) || p0 < 0 || p1 < 0) {
+            if (t.t0 + 32 > sp.n || (t.t0 < sp.lo && t.t0 + 32 > a.sinks) ||
+                (t.page[0] | t.page[1]) < 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int t = t0 + 16 * h + 4 * g + r;
-                        const bool see = t < sp.n && (t >= sp.lo || t < a.sinks) &&
-                                         (h ? p1 : p0) >= 0;
+                        const int j = t.t0 + 16 * h + 4 * g + r;
+                        const bool see = j < sp.n && (j >= sp.lo || j < a.sinks) && t.page[h] >= 0;
                         if (!see) {
                             x[h][r] = -INFINITY;
-                            v[h][r].zero();
-                            if constexpr (INT8) vs[h][r] = 0.0f;
+                            t.v[h][r].zero();
+                            if constexpr (INT8) t.vs[h][r] = 0.0f;
                         }
                     }
             }
@@ -336,16 +389,25 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
                 for (int r = 0; r < 4; ++r) {
                     const float e = __builtin_amdgcn_exp2f(x[h][r] - mu);
                     l += e;
-                    p[4 * h + r] = INT8 ? e * vs[h][r] : e;
+                    p[4 * h + r] = INT8 ? e * t.vs[h][r] : e;
                 }
             uint4 pb[kP];
             split_bf16<kP>(p, pb);
 #pragma unroll
             for (int e = 0; e < VD; ++e) {
-                const uint4 vt = {pair(v[0][0], v[0][1], e), pair(v[0][2], v[0][3], e),
-                                  pair(v[1][0], v[1][1], e), pair(v[1][2], v[1][3], e)};
+                const uint4 vt = {pair(t.v[0][0], t.v[0][1], e), pair(t.v[0][2], t.v[0][3], e),
+                                  pair(t.v[1][0], t.v[1][1], e), pair(t.v[1][2], t.v[1][3], e)};
 #pragma unroll
-                for (int t = kP - 1; t >= 0; --t) o[e] = mfma16(vt, pb[t], o[e]);
+                for (int u = kP - 1; u >= 0; --u) o[e] = mfma16(vt, pb[u], o[e]);
+            }
+        };
+        int i = u0 * NW + wave;
+        if (i < last) {
+            look_up(i);
+            Tile<DP, INT8> t;
+            for (; i < last; i += NW) {
+                load(t, i);
+                compute(t);
             }
         }
 
@@ -359,7 +421,7 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
         for (int w = 1; w < NW; ++w) mx = fmaxf(mx, sm[w * 16 + c]);
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
         if (c < rows) {
-            float *to = lds + (wave * hd.rows + c) * kRow + g * 4 * VD;
+            float *to = join + (wave * hd.rows + c) * kRow + g * 4 * VD;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -382,7 +444,7 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
                 const float mw = sm[w * 16 + r];
                 lr += mw == -INFINITY ? 0.0f : sl[w * 16 + r] * __builtin_amdgcn_exp2f(mw - mr);
                 const float4 z =
-                    *reinterpret_cast<const float4 *>(lds + (w * hd.rows + r) * kRow + d);
+                    *reinterpret_cast<const float4 *>(join + (w * hd.rows + r) * kRow + d);
                 y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
             }
             if (SPLIT && !whole) {
@@ -401,6 +463,21 @@ __global__ __launch_bounds__(NW * 64) void k_kv_decode(KvAttnArgs a) {
     }
 }
 
+// (m, l, y) += another part (mk, lk, z) of the same row.
+__device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk, float lk,
+                                         float4 z) {
+    if (mk == -INFINITY) return;
+    const float mn = fmaxf(m, mk);
+    const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+    const float fb = __builtin_amdgcn_exp2f(mk - mn);
+    m = mn;
+    l = l * fa + lk * fb;
+    y.x = y.x * fa + z.x * fb;
+    y.y = y.y * fa + z.y * fb;
+    y.z = y.z * fa + z.z * fb;
+    y.w = y.w * fa + z.w * fb;
+}
+
 // Joins the parts of the (sequence, head) pairs whose units went to more than
 // one workgroup, in the workgroups' order.
 template <int DP, bool FP32, int NW>
@@ -411,37 +488,38 @@ __global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a, int blocks
     int64_t k0, k1;
     kv_blocks_of<NW>(a, hd, b, h, blocks, k0, k1);
     if (k0 == k1) return;
-    const int kvh = h / hd.per_head, part = h % hd.per_head, D = a.c.D;
-    const int rows = min(hd.group - part * 16, 16);
-    for (int at = threadIdx.x; at < rows * (DP / 4); at += 256) {
-        const int r = at / (DP / 4), d = at % (DP / 4) * 4;
-        float m = -INFINITY, l = 0.0f;
-        float4 y = {};
-        for (int64_t k = k0; k <= k1; ++k) {
-            const KvPartial p(a, hd, DP, k * 2 + (k == k0));
-            const float mk = p.m[r];
-            const float4 z = *reinterpret_cast<const float4 *>(p.o + r * DP + d);
-            if (mk == -INFINITY) continue;
-            const float mn = fmaxf(m, mk);
-            const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
-            const float fb = __builtin_amdgcn_exp2f(mk - mn);
-            m = mn;
-            l = l * fa + p.l[r] * fb;
-            y.x = y.x * fa + z.x * fb;
-            y.y = y.y * fa + z.y * fb;
-            y.z = y.z * fa + z.z * fb;
-            y.w = y.w * fa + z.w * fb;
-        }
-        if (d < D)
-            store_out<FP32>(a.out, (b * a.hq + (int64_t)kvh * hd.group + part * 16 + r) * D + d, y,
-                            l);
+    const int kvh = h / hd.per_head, part = h % hd.per_head, D = a.c.D, r = blockIdx.y;
+    if (r >= min(hd.group - part * 16, 16)) return;
+    // DP / 4 threads have a row's values, 4 each; kGroups of them take parts in turn
+    constexpr int kLanes = DP / 4, kGroups = 256 / kLanes;
+    __shared__ float4 so[kGroups][kLanes];
+    __shared__ float sm[kGroups], sl[kGroups];
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    float m = -INFINITY, l = 0.0f;
+    float4 y = {};
+    for (int64_t k = k0 + grp; k <= k1; k += kGroups) {
+        const KvPartial p(a, hd, DP, k * 2 + (k == k0));
+        add_part(m, l, y, p.m[r], p.l[r], *reinterpret_cast<const float4 *>(p.o + r * DP + d));
     }
+    so[grp][threadIdx.x % kLanes] = y;
+    if (d == 0) sm[grp] = m, sl[grp] = l;
+    __syncthreads();
+    if (grp != 0 || d >= D) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) add_part(m, l, y, sm[i], sl[i], so[i][threadIdx.x % kLanes]);
+    store_out<FP32>(a.out, (b * a.hq + (int64_t)kvh * hd.group + part * 16 + r) * D + d, y, l);
 }
 
 namespace {
 
-constexpr int kSplitWaves = 4, kWholeWaves = 8, kSplitBlocks = 1024;
+constexpr int kSplitWaves = 4, kSplitBlocks = KV_BLOCKS;
 constexpr int64_t kWholeTokens = 2048;
+
+template <int DP, bool INT8>
+size_t lds_bytes(int waves, int rows) {
+    const int join = rows * (DP + 4) * 4, stage = 16 * DP * (INT8 ? 1 : 2);
+    return (size_t)waves * (std::max(join, stage) + 2 * 16 * 4);
+}
 
 template <int DP, bool INT8, bool FP32>
 hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
@@ -451,14 +529,15 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     int64_t most = a.c.W << a.c.shift;
     if (a.window) most = std::min<int64_t>(most, (int64_t)a.window + a.sinks + 64);
     if (most <= kWholeTokens) {
-        const size_t lds = (size_t)kWholeWaves * (hd.rows * (DP + 4) + 32) * 4;
+        constexpr int kWholeWaves = DP == 256 && FP32 ? 4 : 8;  // (registers)
+        const size_t lds = lds_bytes<DP, INT8>(kWholeWaves, hd.rows);
         auto *k = k_kv_decode<DP, INT8, FP32, kWholeWaves, false>;
         hipLaunchKernelGGL(k, dim3((unsigned)pairs), dim3(kWholeWaves * 64), lds, st, a);
     } else {
-        const size_t lds = (size_t)kSplitWaves * (hd.rows * (DP + 4) + 32) * 4;
+        const size_t lds = lds_bytes<DP, INT8>(kSplitWaves, hd.rows);
         auto *k = k_kv_decode<DP, INT8, FP32, kSplitWaves, true>;
         hipLaunchKernelGGL(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
-        hipLaunchKernelGGL((k_kv_decode_join<DP, FP32, kSplitWaves>), dim3((unsigned)pairs),
+        hipLaunchKernelGGL((k_kv_decode_join<DP, FP32, kSplitWaves>), dim3((unsigned)pairs, hd.rows),
                            dim3(256), 0, st, a, (int)kSplitBlocks);
     }
     return hipGetLastError();
