@@ -25,16 +25,20 @@
 // (24 significant bits), each its own MFMA into the same fp32 accumulator; K
 // and V are exact in bf16 (int8 codes have 8 bits), so products keep fp32
 // accuracy.  bf16 activations: q is exact, the weights keep two terms (16
-// bits), so that the output's own rounding dominates.
+// bits), so that the output's own rounding dominates.  Where the group's rows
+// leave columns free (4 rows of 3 terms, 8 rows of 2), the terms take columns
+// of their own: one MFMA for all of them, and the columns are summed at the end.
 #include "kv_attn.h"
 
 namespace w4 {
 
 #ifndef KV_WAVES
-#define KV_WAVES (DP == 256 ? (FP32 ? 1 : 2) : DP == 128 && FP32 && !INT8 ? 2 : 3)
+#define KV_WAVES (DP == 256 ? (FP32 && !PACK ? 1 : 2) : DP == 128 ? (FP32 && !PACK && !INT8 ? 2 : 3) : 4)
 #define KV_BLOCKS 768
 #endif
 namespace {
+
+constexpr int kRowRor4 = 0x124;  // row_ror:4
 
 __device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
@@ -94,6 +98,39 @@ __device__ __forceinline__ uint32_t pair(const Piece<INT8, VD> &x, const Piece<I
         return code_pair((int8_t)(x.w[e / 4] >> (e % 4 * 8)), (int8_t)(y.w[e / 4] >> (e % 4 * 8)));
     else
         return __builtin_amdgcn_perm(y.w[e / 2], x.w[e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// Sum over the 16 / N groups of N columns (N = 4, 8); every lane gets it, with
+// the same bits in every group.
+template <int N>
+__device__ __forceinline__ float sum_columns(float v) {
+    v += __int_as_float(dpp<kRowRor8>(__float_as_int(v)));
+    if constexpr (N == 4) v += __int_as_float(dpp<kRowRor4>(__float_as_int(v)));
+    return v;
+}
+
+// Term `term` of the split_bf16 of eight floats (zeros from N on): every lane
+// its own, by leaving out the subtractions behind it.
+template <int N>
+__device__ __forceinline__ uint4 term_bf16(const float (&f)[8], int term) {
+    float r[8];
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = f[j];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const float on = t < term ? -1.0f : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = pack_bf16(r[2 * j], r[2 * j + 1]);
+            if (t + 1 < N) {
+                r[2 * j] = __builtin_fmaf(on, bf16_lo(w[j]), r[2 * j]);
+                r[2 * j + 1] = __builtin_fmaf(on, bf16_hi(w[j]), r[2 * j + 1]);
+            }
+        }
+    }
+    const bool none = term >= N;
+    return uint4{none ? 0 : w[0], none ? 0 : w[1], none ? 0 : w[2], none ? 0 : w[3]};
 }
 
 // A wave's 32 tokens.
@@ -231,15 +268,18 @@ struct KvPartial {
 }  // namespace
 
 // DP: head_dim rounded up to 64, 128 or 256 (values beyond head_dim: q is zero
-// there, and their V rows are not stored).  NW: waves.  SPLIT: the workgroups
-// share all units of work evenly (see unit_range), else workgroup i has all of
+// there, and their V rows are not stored).  PACK: few rows (4 with fp32
+// activations, 8 with bf16), whose terms share the 16 columns.  NW: waves.  SPLIT: the workgroups
+// share all units of work evenly (see KvCursor), else workgroup i has all of
 // (sequence, head) i.
-template <int DP, bool INT8, bool FP32, int NW, bool SPLIT>
+template <int DP, bool INT8, bool FP32, bool PACK, int NW, bool SPLIT>
 __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
     constexpr int kSteps = DP / 32, VD = DP / 16, kB = INT8 ? 1 : 2;
     constexpr int kLoads = INT8 ? kSteps / 2 : kSteps;
     constexpr int kCh = DP * kB / 16, kRowsPer = 64 / kCh;  // 16-byte chunks of a row, rows of a load
-    constexpr int kQ = FP32 ? 3 : 1, kP = FP32 ? 3 : 2;
+    constexpr int kTerms = FP32 ? 3 : 2;                     // of the softmax weights
+    constexpr int kQ = FP32 && !PACK ? 3 : 1, kP = PACK ? 1 : kTerms;
+    constexpr int kGroup = PACK ? (FP32 ? 4 : 8) : 16;      // columns of one term
     constexpr int kRow = DP + 4;  // LDS row of the join, padded off the banks
     extern __shared__ float lds[];
     const int lane = threadIdx.x % kWave, c = lane % 16, g = lane / 16;
@@ -265,12 +305,26 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
         const int rows = min(hd.group - part * 16, 16);
         const int64_t qrow = b * a.ldq + ((int64_t)kvh * hd.group + part * 16) * D;
 
-        // q as the B operand: lane c holds row c, group g its share of each 32 dims
+        // q as the B operand: lane c holds row c, group g its share of each 32 dims;
+        // packed, lane c holds term c / kGroup of row c % kGroup
+        const int term = c / kGroup, qr = c % kGroup;
         uint4 q[kQ][kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int d = INT8 ? s / 2 * 64 + g * 16 + s % 2 * 8 : s * 32 + g * 8;
-            load_query<FP32>(a.q, qrow + (int64_t)c * D + d, c < rows && d < D, q, s);
+            if constexpr (FP32 && PACK) {
+                uint4 all[3][1];
+                load_query<FP32>(a.q, qrow + (int64_t)qr * D + d, qr < rows && d < D, all, 0);
+                auto pick = [&](uint32_t t0, uint32_t t1, uint32_t t2) {
+                    return term == 0 ? t0 : term == 1 ? t1 : term == 2 ? t2 : 0u;
+                };
+                q[0][s].x = pick(all[0][0].x, all[1][0].x, all[2][0].x);
+                q[0][s].y = pick(all[0][0].y, all[1][0].y, all[2][0].y);
+                q[0][s].z = pick(all[0][0].z, all[1][0].z, all[2][0].z);
+                q[0][s].w = pick(all[0][0].w, all[1][0].w, all[2][0].w);
+            } else {
+                load_query<FP32>(a.q, qrow + (int64_t)qr * D + d, qr < rows && d < D, q, s);
+            }
         }
         v4f o[VD] = {};
         float m = -INFINITY, l = 0.0f;
@@ -345,7 +399,10 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
                     for (int u = kQ - 1; u >= 0; --u) s4 = mfma16(kk, q[u][s], s4);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[h][r] = s4[r] * (INT8 ? scale2 * t.ks[h][r] : scale2);
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (FP32 && PACK) s4[r] = sum_columns<kGroup>(s4[r]);
+                    x[h][r] = s4[r] * (INT8 ? scale2 * t.ks[h][r] : scale2);
+                }
             }
             // tiles at an edge, or with a page missing: hide tokens, and clear
             // their V, which may hold anything (0 * NaN would stay)
@@ -392,7 +449,10 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
                     p[4 * h + r] = INT8 ? e * t.vs[h][r] : e;
                 }
             uint4 pb[kP];
-            split_bf16<kP>(p, pb);
+            if constexpr (PACK)
+                pb[0] = term_bf16<kTerms>(p, term);
+            else
+                split_bf16<kP>(p, pb);
 #pragma unroll
             for (int e = 0; e < VD; ++e) {
                 const uint4 vt = {pair(t.v[0][0], t.v[0][1], e), pair(t.v[0][2], t.v[0][3], e),
@@ -420,6 +480,12 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
 #pragma unroll
         for (int w = 1; w < NW; ++w) mx = fmaxf(mx, sm[w * 16 + c]);
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
+        if constexpr (PACK) {
+#pragma unroll
+            for (int e = 0; e < VD; ++e)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[e][r] = sum_columns<kGroup>(o[e][r]);
+        }
         if (c < rows) {
             float *to = join + (wave * hd.rows + c) * kRow + g * 4 * VD;
 #pragma unroll
@@ -521,7 +587,7 @@ size_t lds_bytes(int waves, int rows) {
     return (size_t)waves * (std::max(join, stage) + 2 * 16 * 4);
 }
 
-template <int DP, bool INT8, bool FP32>
+template <int DP, bool INT8, bool FP32, bool PACK>
 hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     const KvHeads hd(a);
     const int64_t pairs = a.B * hd.count;
@@ -529,13 +595,13 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     int64_t most = a.c.W << a.c.shift;
     if (a.window) most = std::min<int64_t>(most, (int64_t)a.window + a.sinks + 64);
     if (most <= kWholeTokens) {
-        constexpr int kWholeWaves = DP == 256 && FP32 ? 4 : 8;  // (registers)
+        constexpr int kWholeWaves = DP == 256 && FP32 && !PACK ? 4 : 8;  // (registers)
         const size_t lds = lds_bytes<DP, INT8>(kWholeWaves, hd.rows);
-        auto *k = k_kv_decode<DP, INT8, FP32, kWholeWaves, false>;
+        auto *k = k_kv_decode<DP, INT8, FP32, PACK, kWholeWaves, false>;
         hipLaunchKernelGGL(k, dim3((unsigned)pairs), dim3(kWholeWaves * 64), lds, st, a);
     } else {
         const size_t lds = lds_bytes<DP, INT8>(kSplitWaves, hd.rows);
-        auto *k = k_kv_decode<DP, INT8, FP32, kSplitWaves, true>;
+        auto *k = k_kv_decode<DP, INT8, FP32, PACK, kSplitWaves, true>;
         hipLaunchKernelGGL(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
         hipLaunchKernelGGL((k_kv_decode_join<DP, FP32, kSplitWaves>), dim3((unsigned)pairs, hd.rows),
                            dim3(256), 0, st, a, (int)kSplitBlocks);
@@ -543,10 +609,17 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int DP, bool INT8, bool FP32>
+hipError_t launch_group(const KvAttnArgs &a, hipStream_t st) {
+    return a.hq / a.c.heads <= (FP32 ? 4 : 8) ? launch_dp<DP, INT8, FP32, true>(a, st)
+                                              : launch_dp<DP, INT8, FP32, false>(a, st);
+}
+
 template <int DP>
 hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
-    if (a.int8) return a.fp32 ? launch_dp<DP, true, true>(a, st) : launch_dp<DP, true, false>(a, st);
-    return a.fp32 ? launch_dp<DP, false, true>(a, st) : launch_dp<DP, false, false>(a, st);
+    if (a.int8)
+        return a.fp32 ? launch_group<DP, true, true>(a, st) : launch_group<DP, true, false>(a, st);
+    return a.fp32 ? launch_group<DP, false, true>(a, st) : launch_group<DP, false, false>(a, st);
 }
 
 }  // namespace
