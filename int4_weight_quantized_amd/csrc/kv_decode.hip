@@ -32,10 +32,6 @@
 
 namespace w4 {
 
-#ifndef KV_WAVES
-#define KV_WAVES (DP == 256 ? (FP32 && !PACK ? 1 : 2) : DP == 128 ? (FP32 && !PACK && !INT8 ? 2 : 3) : 4)
-#define KV_BLOCKS 768
-#endif
 namespace {
 
 constexpr int kRowRor4 = 0x124;  // row_ror:4
@@ -139,7 +135,14 @@ struct Tile {
     u32x4 k[2][INT8 ? DP / 64 : DP / 32];
     Piece<INT8, DP / 16> v[2][4];
     v4f ks[2], vs[2];
+};
+
+__device__ __forceinline__ int clamp_dim(int d, int D) { return d < D ? d : 0; }
+
+// Where they are: the first token, the pages of its halves and their first vectors.
+struct Place {
     int t0, page[2];
+    int64_t vec[2];
 };
 
 // Byte offset of 16-byte chunk `ch` of row `row` among 16 rows of kCh chunks,
@@ -147,6 +150,21 @@ struct Tile {
 template <int kCh>
 __device__ __forceinline__ int stage_at(int row, int ch) {
     return row * kCh * 16 + ((ch ^ (kCh == 8 ? row >> 1 & 7 : row & 15)) << 4);
+}
+
+// The split kernel: workgroups of 4 waves, 3 a CU of the 256 in one round (512
+// workgroups: 136 us where 768 take 122 and 1536 136; 64 ragged sequences, int8).
+constexpr int kSplitWaves = 4, kSplitBlocks = 768;
+
+// Waves a SIMD that the registers are cut to: as many as K, V, q and O of a
+// wave leave room for without spilling much.
+constexpr int waves_per_simd(int DP, bool INT8, bool FP32, bool PACK) {
+    return DP == 256 ? (FP32 && !PACK ? 1 : 2) : DP == 128 ? (FP32 && !PACK && !INT8 ? 2 : 3) : 4;
+}
+
+template <int NW>
+__device__ __forceinline__ int pair_units(const Span &s) {
+    return max((s.tiles + NW - 1) / NW, 1);
 }
 
 // Query heads in groups of up to 16 that share a cache head: `per_head` groups
@@ -162,27 +180,34 @@ struct KvHeads {
 };
 
 // Work of the split kernel.  A unit is one tile for each of NW waves of one
-// (sequence, head) pair; pairs follow one another, sequence-major, and the U
-// units of all pairs are dealt to the first n = min(workgroups, U) workgroups in
-// equal runs: workgroup k has units floor(k U / n) to floor((k + 1) U / n),
-// whatever the lengths are.  A sequence without tokens has one unit (its outputs are zeros).
+// (sequence, head) pair; a pair costs its units and kStart more (its start and
+// its join keep a workgroup about as long; 0, 1, 2, 3, 4: 122, 113, 105, 106, 110
+// us on 64 ragged sequences).  Pairs follow one
+// another, sequence-major, and the cost U of all of them is dealt to the first
+// n = min(workgroups, U) workgroups in equal runs: workgroup k has the places
+// floor(k U / n) to floor((k + 1) U / n), whatever the lengths are; the first
+// kStart places of a pair hold no unit.  A sequence without tokens has one
+// unit (its outputs are zeros).
+constexpr int kStart = 2;
+
 struct KvCursor {
-    int64_t b;  // the pair
-    int h, u;      // the head, the first unit of the pair
-    int64_t left;  // units left of the run
+    int64_t b;     // the pair
+    int h, at;     // the head, the first place of the pair
+    int left;      // places left of the run
 };
 
-template <int NW>
-__device__ __forceinline__ int64_t pair_units(const KvAttnArgs &a, int64_t b) {
-    return max((make_span(a, b).tiles + NW - 1) / NW, 1);
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// Units of a pair of sequence b0 + lane, and their running sum over the lanes.
+// Cost of a pair of sequence b0 + lane, and the running sum over the lanes.
 template <int NW>
-__device__ __forceinline__ int64_t scan_units(const KvAttnArgs &a, int64_t b0, int64_t &units) {
+__device__ __forceinline__ int64_t scan_cost(const KvAttnArgs &a, int64_t b0, int &cost) {
     const int lane = threadIdx.x % kWave;
-    units = b0 + lane < a.B ? pair_units<NW>(a, b0 + lane) : 0;
-    int64_t s = units;
+    cost = b0 + lane < a.B ? pair_units<NW>(make_span(a, b0 + lane)) + kStart : 0;
+    int64_t s = cost;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
         const int64_t t = __shfl_up(s, o, kWave);
@@ -191,41 +216,31 @@ __device__ __forceinline__ int64_t scan_units(const KvAttnArgs &a, int64_t b0, i
     return s;
 }
 
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
-// Units of all pairs (wave-uniform).
-template <int NW>
-__device__ __forceinline__ int64_t all_units(const KvAttnArgs &a, const KvHeads &hd) {
-    int64_t sum = 0, units;
-    for (int64_t b0 = 0; b0 < a.B; b0 += kWave)
-        sum += __shfl(scan_units<NW>(a, b0, units), kWave - 1, kWave);
-    return uniform(sum) * hd.count;
-}
-
 template <int NW>
 __device__ __forceinline__ KvCursor kv_first_segment(const KvAttnArgs &a, const KvHeads &hd,
                                                      int64_t k, int64_t n) {
-    const int64_t U = all_units<NW>(a, hd);
+    int64_t s = 0, U = 0, before = 0;
+    int cost = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kWave) {
+        s = scan_cost<NW>(a, b0, cost);
+        U += uniform(__shfl(s, kWave - 1, kWave));
+    }
+    U *= hd.count;
     n = min(n, U);
     if (k >= n) return KvCursor{0, 0, 0, 0};
     const int64_t first = k * U / n, last = (k + 1) * U / n;
-    KvCursor cur{0, 0, 0, last - first};
-    int64_t before = 0, units;
+    KvCursor cur{0, 0, 0, (int)(last - first)};
     for (int64_t b0 = 0; b0 < a.B; b0 += kWave) {
-        const int64_t s = scan_units<NW>(a, b0, units);
-        // the first sequence whose units end behind `first`
+        if (a.B > kWave) s = scan_cost<NW>(a, b0, cost);
+        // the first sequence whose places end behind `first`
         const uint64_t hit = __ballot((before + s) * hd.count > first);
         if (hit) {
             const int at = __ffsll((unsigned long long)hit) - 1;
-            const int64_t un = uniform(__shfl(units, at, kWave));
-            const int64_t off = first - (before + uniform(__shfl(s, at, kWave)) - un) * hd.count;
+            const int c = __builtin_amdgcn_readlane(cost, at);
+            const int64_t off = first - (before + uniform(__shfl(s, at, kWave)) - c) * hd.count;
             cur.b = b0 + at;
-            cur.h = (int)(off / un);
-            cur.u = (int)(off - cur.h * un);
+            cur.h = (int)(off / c);
+            cur.at = (int)(off - (int64_t)cur.h * c);
             return cur;
         }
         before += uniform(__shfl(s, kWave - 1, kWave));
@@ -234,35 +249,27 @@ __device__ __forceinline__ KvCursor kv_first_segment(const KvAttnArgs &a, const 
     return cur;
 }
 
-// The first and last workgroup of n that have units of pair (b, h).
-template <int NW>
-__device__ __forceinline__ void kv_blocks_of(const KvAttnArgs &a, const KvHeads &hd, int64_t b,
-                                             int h, int64_t n, int64_t &k0, int64_t &k1) {
-    int64_t U = 0, first = 0, un = 1, units;
-    for (int64_t b0 = 0; b0 < a.B; b0 += kWave) {
-        const int64_t s = scan_units<NW>(a, b0, units);
-        if (b >= b0 && b < b0 + kWave) {
-            un = uniform(__shfl(units, (int)(b - b0), kWave));
-            first = (U + uniform(__shfl(s, (int)(b - b0), kWave)) - un) * hd.count + h * un;
-        }
-        U += uniform(__shfl(s, kWave - 1, kWave));
-    }
-    U *= hd.count;
-    n = min(n, U);
-    k0 = ((first + 1) * n - 1) / U;
-    k1 = ((first + un) * n - 1) / U;
-}
-
 // The part of a pair that a workgroup leaves in the workspace: unnormalized
 // sums, maxima and sums of weights.  Slot 2 k + 1: workgroup k's part that
 // starts a pair, slot 2 k: one that does not.
 struct KvPartial {
     float *o, *m, *l;
     __device__ KvPartial(const KvAttnArgs &a, const KvHeads &hd, int DP, int64_t slot) {
-        o = reinterpret_cast<float *>(a.ws) + slot * hd.rows * (DP + 2);
+        o = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + kSplitBlocks * 16) +
+            slot * hd.rows * (DP + 4);
         m = o + hd.rows * DP;
         l = m + hd.rows;
     }
+};
+
+// At the workspace's start, for each workgroup: whether it has the first units of
+// a pair, but not its last ones (then the pair), and whether its run begins with
+// the last units of a pair that it did not start.  The workgroups between these
+// two have nothing but units of that pair.
+constexpr int kStarts = 1, kEnds = 2;
+struct KvSplitPair {
+    int64_t b;
+    int h, flags;
 };
 
 }  // namespace
@@ -273,7 +280,8 @@ struct KvPartial {
 // share all units of work evenly (see KvCursor), else workgroup i has all of
 // (sequence, head) i.
 template <int DP, bool INT8, bool FP32, bool PACK, int NW, bool SPLIT>
-__global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
+__global__ __launch_bounds__(
+    NW * 64, waves_per_simd(DP, INT8, FP32, PACK)) void k_kv_decode(KvAttnArgs a) {
     constexpr int kSteps = DP / 32, VD = DP / 16, kB = INT8 ? 1 : 2;
     constexpr int kLoads = INT8 ? kSteps / 2 : kSteps;
     constexpr int kCh = DP * kB / 16, kRowsPer = 64 / kCh;  // 16-byte chunks of a row, rows of a load
@@ -295,12 +303,15 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
 
     KvCursor cur = SPLIT ? kv_first_segment<NW>(a, hd, blockIdx.x, gridDim.x)
                          : KvCursor{(int64_t)blockIdx.x / hd.count, (int)(blockIdx.x % hd.count),
-                                    0, (int64_t)1 << 40};
+                                    0, 0x7FFFFFFF};
+    KvSplitPair mark{0, 0, 0};
     while (cur.left > 0) {
         const int64_t b = cur.b;
         const Span sp = make_span(a, b);
-        const int units = max((sp.tiles + NW - 1) / NW, 1);
-        const int u0 = cur.u, u1 = (int)min((int64_t)units, u0 + cur.left);
+        const int units = pair_units<NW>(sp);
+        const int end = min(units + kStart - cur.at, cur.left) + cur.at;
+        const int u0 = max(cur.at - kStart, 0), u1 = max(end - kStart, 0);
+        if (u0 == u1) break;  // (the run ends in front of the pair's first unit)
         const int kvh = cur.h / hd.per_head, part = cur.h % hd.per_head;
         const int rows = min(hd.group - part * 16, 16);
         const int64_t qrow = b * a.ldq + ((int64_t)kvh * hd.group + part * 16) * D;
@@ -341,43 +352,51 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
             base = i;
             pages = ii < last ? kv_page(a.c, table, tile_token(ii) + lane % 2 * 16) : -1;
         };
-        auto load = [&](Tile<DP, INT8> &t, int i) {
+        Place now;
+        auto place = [&](Place &p, int i) {
             if (i - base >= 32 * NW) look_up(i);
             const int at = (i - base) / NW * 2;
-            t.t0 = tile_token(i);
-            t.page[0] = __builtin_amdgcn_readlane(pages, at);
-            t.page[1] = __builtin_amdgcn_readlane(pages, at + 1);
+            p.t0 = tile_token(i);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t vec = kv_vector(a.c, max(t.page[h], 0), kvh, t.t0 + 16 * h);
-#pragma unroll
-                for (int s = 0; s < kLoads; ++s) {
-                    // whole rows one after another (rows of 64 bytes: one load
-                    // has all 16, each lane its own place of the A operand)
-                    const int row = kCh > 4 ? s * kRowsPer + lane / kCh : c;
-                    const int d = (kCh > 4 ? lane % kCh : g) * (16 / kB);
-                    t.k[h][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(
-                        a.c.k + ((vec + row) * D + (d < D ? d : 0)) * kB));
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t vec = kv_vector(a.c, max(t.page[h], 0), kvh, t.t0 + 16 * h) + g * 4;
-                const uint8_t *vp = a.c.v + vec * D * kB + (c * VD < D ? c * VD : 0) * kB;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) t.v[h][j].load(vp + j * D * kB);
-                if constexpr (INT8) {
-                    t.ks[h] = *reinterpret_cast<const v4f *>(a.c.ks + vec);
-                    t.vs[h] = *reinterpret_cast<const v4f *>(a.c.vs + vec);
-                }
+                p.page[h] = __builtin_amdgcn_readlane(pages, at + h);
+                p.vec[h] = kv_vector(a.c, max(p.page[h], 0), kvh, p.t0 + 16 * h);
             }
         };
-        auto compute = [&](Tile<DP, INT8> &t) {
+        Tile<DP, INT8> t;
+        // (a uniform address and a lane's 32-bit offset in a page: whole rows one
+        // after another; rows of 64 bytes: one load has all 16, each lane its own
+        // place of the A operand)
+        const uint32_t k_off = ((kCh > 4 ? lane / kCh : c) * D + clamp_dim(
+                                    (kCh > 4 ? lane % kCh : g) * (16 / kB), D)) * kB;
+        const uint32_t v_off = (g * 4 * D + clamp_dim(c * VD, D)) * kB;
+        auto load_k = [&](const Place &p, int h) {
+            const uint8_t *at = a.c.k + p.vec[h] * (D * kB);
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s, at += kRowsPer * D * kB)
+                t.k[h][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at + k_off));
+        };
+        auto load_ks = [&](const Place &p, int h) {
+            if constexpr (INT8)
+                t.ks[h] = *reinterpret_cast<const v4f *>(a.c.ks + p.vec[h] + (uint32_t)(g * 4));
+        };
+        auto load_v = [&](const Place &p) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *at = a.c.v + p.vec[h] * (D * kB);
+                if constexpr (INT8)
+                    t.vs[h] = *reinterpret_cast<const v4f *>(a.c.vs + p.vec[h] + (uint32_t)(g * 4));
+#pragma unroll
+                for (int j = 0; j < 4; ++j, at += D * kB) t.v[h][j].load(at + v_off);
+            }
+        };
+        auto compute = [&]() {
             float x[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // rows -> the A operand (lane: row c, chunk 4 s + g) through this
                 // wave's LDS; a wave's LDS operations are in order
+                u32x4 ka[kLoads];
                 if constexpr (kCh > 4) {
 #pragma unroll
                     for (int s = 0; s < kLoads; ++s)
@@ -386,14 +405,15 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
                     for (int s = 0; s < kLoads; ++s)
-                        t.k[h][s] =
-                            *reinterpret_cast<const u32x4 *>(stage + stage_at<kCh>(c, 4 * s + g));
+                        ka[s] = *reinterpret_cast<const u32x4 *>(stage + stage_at<kCh>(c, 4 * s + g));
                     __builtin_amdgcn_wave_barrier();
+                } else {
+                    ka[0] = t.k[h][0];
                 }
                 v4f s4 = {};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const uint4 raw = __builtin_bit_cast(uint4, t.k[h][INT8 ? s / 2 : s]);
+                    const uint4 raw = __builtin_bit_cast(uint4, ka[INT8 ? s / 2 : s]);
                     const uint4 kk = INT8 ? codes8(raw, s % 2) : raw;
 #pragma unroll
                     for (int u = kQ - 1; u >= 0; --u) s4 = mfma16(kk, q[u][s], s4);
@@ -406,14 +426,15 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
             }
             // tiles at an edge, or with a page missing: hide tokens, and clear
             // their V, which may hold anything (0 * NaN would stay)
-            if (t.t0 + 32 > sp.n || (t.t0 < sp.lo && t.t0 + 32 > a.sinks) ||
-                (t.page[0] | t.page[1]) < 0) {
+            if (now.t0 + 32 > sp.n || (now.t0 < sp.lo && now.t0 + 32 > a.sinks) ||
+                (now.page[0] | now.page[1]) < 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int j = t.t0 + 16 * h + 4 * g + r;
-                        const bool see = j < sp.n && (j >= sp.lo || j < a.sinks) && t.page[h] >= 0;
+                        const int j = now.t0 + 16 * h + 4 * g + r;
+                        const bool see =
+                            j < sp.n && (j >= sp.lo || j < a.sinks) && now.page[h] >= 0;
                         if (!see) {
                             x[h][r] = -INFINITY;
                             t.v[h][r].zero();
@@ -464,10 +485,12 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
         int i = u0 * NW + wave;
         if (i < last) {
             look_up(i);
-            Tile<DP, INT8> t;
             for (; i < last; i += NW) {
-                load(t, i);
-                compute(t);
+                place(now, i);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) load_k(now, h), load_ks(now, h);
+                load_v(now);
+                compute();
             }
         }
 
@@ -497,6 +520,8 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
         }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;
+        if (SPLIT && u0 == 0 && u1 < units) mark = KvSplitPair{b, cur.h, mark.flags | kStarts};
+        if (SPLIT && u0 > 0 && u1 == units) mark.flags |= kEnds;
         const KvPartial part_ws(a, hd, DP, (int64_t)blockIdx.x * 2 + (u0 == 0));
         for (int at = threadIdx.x; at < rows * (DP / 4); at += NW * 64) {
             const int r = at / (DP / 4), d = at % (DP / 4) * 4;
@@ -523,10 +548,11 @@ __global__ __launch_bounds__(NW * 64, KV_WAVES) void k_kv_decode(KvAttnArgs a) {
         }
         __syncthreads();
         if (!SPLIT) break;
-        cur.left -= u1 - u0;
-        cur.u = 0;
+        cur.left -= end - cur.at;
+        cur.at = 0;
         if (++cur.h == hd.count) cur.h = 0, ++cur.b;
     }
+    if (SPLIT && threadIdx.x == 0) reinterpret_cast<KvSplitPair *>(a.ws)[blockIdx.x] = mark;
 }
 
 // (m, l, y) += another part (mk, lk, z) of the same row.
@@ -544,17 +570,23 @@ __device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk
     y.w = y.w * fa + z.w * fb;
 }
 
-// Joins the parts of the (sequence, head) pairs whose units went to more than
-// one workgroup, in the workgroups' order.
-template <int DP, bool FP32, int NW>
-__global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a, int blocks) {
+// Joins the parts of the pair that workgroup blockIdx.x of the split kernel
+// started and others went on with, in the workgroups' order.
+template <int DP, bool FP32>
+__global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a) {
     const KvHeads hd(a);
-    const int64_t b = blockIdx.x / hd.count;
-    const int h = (int)(blockIdx.x % hd.count);
-    int64_t k0, k1;
-    kv_blocks_of<NW>(a, hd, b, h, blocks, k0, k1);
-    if (k0 == k1) return;
-    const int kvh = h / hd.per_head, part = h % hd.per_head, D = a.c.D, r = blockIdx.y;
+    const KvSplitPair *marks = reinterpret_cast<const KvSplitPair *>(a.ws);
+    const KvSplitPair sp = marks[blockIdx.x];
+    if (!(sp.flags & kStarts)) return;
+    int parts = 1;  // up to the workgroup with the pair's last units
+    for (int k = blockIdx.x + 1; k < kSplitBlocks; k += kWave) {
+        const int kk = k + threadIdx.x % kWave;
+        const uint64_t hit = __ballot(kk < kSplitBlocks && marks[kk].flags & kEnds);
+        parts += hit ? __ffsll((unsigned long long)hit) : kWave;
+        if (hit) break;
+    }
+    const int64_t b = sp.b;
+    const int kvh = sp.h / hd.per_head, part = sp.h % hd.per_head, D = a.c.D, r = blockIdx.y;
     if (r >= min(hd.group - part * 16, 16)) return;
     // DP / 4 threads have a row's values, 4 each; kGroups of them take parts in turn
     constexpr int kLanes = DP / 4, kGroups = 256 / kLanes;
@@ -563,8 +595,8 @@ __global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a, int blocks
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
     float m = -INFINITY, l = 0.0f;
     float4 y = {};
-    for (int64_t k = k0 + grp; k <= k1; k += kGroups) {
-        const KvPartial p(a, hd, DP, k * 2 + (k == k0));
+    for (int i = grp; i < parts; i += kGroups) {
+        const KvPartial p(a, hd, DP, ((int64_t)blockIdx.x + i) * 2 + (i == 0));
         add_part(m, l, y, p.m[r], p.l[r], *reinterpret_cast<const float4 *>(p.o + r * DP + d));
     }
     so[grp][threadIdx.x % kLanes] = y;
@@ -578,7 +610,6 @@ __global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a, int blocks
 
 namespace {
 
-constexpr int kSplitWaves = 4, kSplitBlocks = KV_BLOCKS;
 constexpr int64_t kWholeTokens = 2048;
 
 template <int DP, bool INT8>
@@ -603,8 +634,8 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
         const size_t lds = lds_bytes<DP, INT8>(kSplitWaves, hd.rows);
         auto *k = k_kv_decode<DP, INT8, FP32, PACK, kSplitWaves, true>;
         hipLaunchKernelGGL(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
-        hipLaunchKernelGGL((k_kv_decode_join<DP, FP32, kSplitWaves>), dim3((unsigned)pairs, hd.rows),
-                           dim3(256), 0, st, a, (int)kSplitBlocks);
+        hipLaunchKernelGGL((k_kv_decode_join<DP, FP32>), dim3(kSplitBlocks, hd.rows), dim3(256), 0,
+                           st, a);
     }
     return hipGetLastError();
 }
@@ -627,7 +658,7 @@ hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
 size_t kv_decode_ws_bytes(int64_t hq, int64_t heads, int64_t D) {
     const int64_t rows = std::min<int64_t>(hq / heads, 16);
     const int64_t DP = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    return (size_t)(kSplitBlocks * 2 * rows * (DP + 2) * 4);
+    return (size_t)(kSplitBlocks * (16 + 2 * rows * (DP + 4) * 4));
 }
 
 hipError_t launch_kv_decode(const KvAttnArgs &a, hipStream_t st) {

@@ -58,7 +58,23 @@ SIGNATURES = {
     "kv_compact": ([_P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _N),
 }
 
-from . import _check, _dev, _opt, _stream, lib  # noqa: E402  (the package's helpers, defined before this import)
+from . import _check, _dev, _opt, _stream as _stream_handle, lib  # noqa: E402  (the package's helpers, defined before this import)
+
+
+def _stream(stream, dev) -> int:
+    """Handle of `stream`, or of the current stream of the call's device
+    (without the Stream object of torch.cuda.current_stream, 2.7 us a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream_handle(stream)
+
+
+def _ptr(t, name, dtype, shape, dev) -> int:
+    """_dev with its checks in one expression; _dev itself names what is wrong."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        return t.data_ptr()
+    return _dev(t, name, dtype, shape, dev)
 
 
 class KVCache:
@@ -85,6 +101,9 @@ class KVCache:
                          _opt(v_scale, "v_scale", torch.float32, shape[:4], dev), *shape,
                          KV_INT8 if int8 else KV_BF16)
         self._ref = ctypes.addressof(self._c)
+        # workspace of the page moves (calls that move this cache's pages are in
+        # order anyway: they write the same pages, tables and counts)
+        self._moves = torch.empty((16 * self.pages + 256,), dtype=torch.uint8, device=dev)
 
     @classmethod
     def empty(cls, layers: int, pages: int, heads: int, page_size: int, head_dim: int,
@@ -107,8 +126,8 @@ def _table(table: torch.Tensor, rows, dev):
     """(pointer, rows, row width) of a page table."""
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a 2-D tensor [sequences, pages of a sequence]")
-    return _dev(table, "table", torch.int32, None if rows is None else (rows, table.shape[1]),
-                dev), table.shape[0], table.shape[1]
+    n, W = table.shape
+    return _ptr(table, "table", torch.int32, (n if rows is None else rows, W), dev), n, W
 
 
 def _rows(x: torch.Tensor, name: str, heads, head_dim: int, dev, dtype=None):
@@ -136,13 +155,13 @@ def _empty(shape, dtype, dev, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+        stream = torch.cuda.ExternalStream(_stream(stream, dev), device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _int32(t, name, n, dev):
-    return _dev(t, name, torch.int32, (n,), dev)
+    return _ptr(t, name, torch.int32, (n,), dev)
 
 
 def kv_append(cache: KVCache, layer: int, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -160,8 +179,8 @@ def kv_append(cache: KVCache, layer: int, k: torch.Tensor, v: torch.Tensor, tabl
     pt, B, W = _table(table, None, dev)
     _check("kv_append", lib().kv_append(
         c._ref, layer, pk, pv, _XTYPES[k.dtype], ldk, ldv, T, B, pt, W,
-        _int32(start, "start", B, dev), _opt(cu, "cu", torch.int32, (B + 1,), dev),
-        _stream(stream)))
+        _int32(start, "start", B, dev), None if cu is None else _int32(cu, "cu", B + 1, dev),
+        _stream(stream, dev)))
 
 
 def kv_gather(cache: KVCache, layer: int, table: torch.Tensor, start: torch.Tensor,
@@ -177,9 +196,9 @@ def kv_gather(cache: KVCache, layer: int, table: torch.Tensor, start: torch.Tens
     v = _empty(shape, dtype, dev, stream) if v is None else v
     pt, B, W = _table(table, None, dev)
     _check("kv_gather", lib().kv_gather(
-        c._ref, layer, _dev(k, "k", dtype, shape, dev), _dev(v, "v", dtype, shape, dev),
+        c._ref, layer, _ptr(k, "k", dtype, shape, dev), _ptr(v, "v", dtype, shape, dev),
         _XTYPES[dtype], tokens, B, pt, W, _int32(start, "start", B, dev),
-        _opt(cu, "cu", torch.int32, (B + 1,), dev), _stream(stream)))
+        None if cu is None else _int32(cu, "cu", B + 1, dev), _stream(stream, dev)))
     return k, v
 
 
@@ -197,14 +216,15 @@ def _attention(name, q, cache, layer, table, lens, cu, scale, window, sinks, out
     T, hq, D = q.shape
     pt, B, W = _table(table, T if cu is None else None, dev)
     if out is None:
-        out = _empty((T, hq, D), q.dtype, dev, stream)
+        out = (torch.empty_like(q) if stream is None and q.is_contiguous()
+               else _empty((T, hq, D), q.dtype, dev, stream))
     if workspace is None:
         need = kv_attention_workspace_bytes(T, B, hq, c.heads, D)
         workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
     rest = (1.0 / math.sqrt(D) if scale is None else scale, window, sinks,
-            _dev(out, "out", q.dtype, (T, hq, D), dev),
-            _dev(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
-            _stream(stream))
+            _ptr(out, "out", q.dtype, (T, hq, D), dev),
+            _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),
+            _stream(stream, dev))
     if cu is None:
         rc = lib().kv_decode_attention(c._ref, layer, pq, _XTYPES[q.dtype], ldq, T, hq, pt, W,
                                        _int32(lens, "lens", B, dev), *rest)
@@ -249,13 +269,14 @@ def kv_copy_pages(dst: KVCache, dst_ids: torch.Tensor, src: KVCache, src_ids: to
     n = dst_ids.numel()
     _check("kv_copy_pages", lib().kv_copy_pages(
         d._ref, _int32(dst_ids, "dst_ids", n, d.device), s._ref,
-        _int32(src_ids, "src_ids", n, d.device), n, _stream(stream)))
+        _int32(src_ids, "src_ids", n, d.device), n, _stream(stream, d.device)))
 
 
-def _work(workspace, need, dev, stream):
+def _work(workspace, need, dev, stream, kept=None):
     if workspace is None:
-        workspace = _empty((need,), torch.uint8, dev, stream)
-    return workspace, _dev(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
+        workspace = (kept if kept is not None and kept.numel() >= need
+                     else _empty((need,), torch.uint8, dev, stream))
+    return workspace, _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
 
 
 def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, add: torch.Tensor,
@@ -269,7 +290,7 @@ def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, add:
     _check("kv_reserve", lib().kv_reserve(
         pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", refs.numel(), dev),
         refs.numel(), page_size, _int32(add, "add", S, dev), _int32(ok, "ok", S, dev),
-        *ws, _stream(stream)))
+        *ws, _stream(stream, dev)))
     return ok
 
 
@@ -283,11 +304,11 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
     pt, S, W = _table(table, None, dev)
     n = parents.numel()
     ok = _empty((n,), torch.int32, dev, stream) if ok is None else ok
-    work, *ws = _work(workspace, 16 * n + 256, dev, stream)
+    work, *ws = _work(workspace, 16 * n + 256, dev, stream, c._moves)
     _check("kv_fork", lib().kv_fork(
         c._ref, pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", c.pages, dev),
         _int32(parents, "parents", n, dev), _int32(children, "children", n, dev), n,
-        _int32(ok, "ok", n, dev), *ws, _stream(stream)))
+        _int32(ok, "ok", n, dev), *ws, _stream(stream, dev)))
     return ok
 
 
@@ -300,7 +321,7 @@ def kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, slots: 
     n = slots.numel()
     _check("kv_free", lib().kv_free(
         pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", refs.numel(), dev),
-        refs.numel(), _int32(slots, "slots", n, dev), n, _stream(stream)))
+        refs.numel(), _int32(slots, "slots", n, dev), n, _stream(stream, dev)))
 
 
 def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor, table_out=None,
@@ -314,10 +335,10 @@ def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor, table_ou
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
     live = _empty((1,), torch.int32, dev, stream) if live is None else live
-    work, *ws = _work(workspace, 8 * c.pages + 256, dev, stream)
+    work, *ws = _work(workspace, 8 * c.pages + 256, dev, stream, c._moves)
     _check("kv_compact", lib().kv_compact(
         c._ref, pt, S, W, _int32(refs, "refs", c.pages, dev),
-        _dev(table_out, "table_out", torch.int32, (S, W), dev),
+        _ptr(table_out, "table_out", torch.int32, (S, W), dev),
         _int32(refs_out, "refs_out", c.pages, dev), _int32(live, "live", 1, dev),
-        *ws, _stream(stream)))
+        *ws, _stream(stream, dev)))
     return table_out, refs_out, live
