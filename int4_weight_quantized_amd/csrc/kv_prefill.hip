@@ -11,14 +11,21 @@
 // v_mfma_f32_32x32x16_bf16: a lane holds one query row throughout, so that
 // maxima, sums and rescaling need one exchange between two lanes, and the
 // accumulators of S^T are the B operand of the second product as they stand
-// (the order of tokens inside its depth is free; V^T is laid out to match).
+// (the order of tokens inside its depth is free; V is read to match).
 //
-// K and V tiles go memory -> registers -> LDS, two LDS buffers, the loads of
-// the next tile in flight during the products of this one, one barrier a tile.
-// K lies row by row, V transposed (4 x VE blocks by byte permutes), both with
-// 16-byte chunks XOR-swizzled so that reads of 16 rows cover all banks once.
-// int8 codes become bf16 on the way to LDS (exact); their scales multiply the
-// scores and the softmax weights.
+// K and V tiles lie in LDS row by row, 16-byte chunks XOR-swizzled so that the
+// reads cover all banks evenly; V^T comes out of its rows by the transposing
+// read ds_read_b64_tr_b16 (16 lanes read 4 rows of 16 values and get a column's
+// 4 each).  A bf16 cache goes to LDS directly (no registers, the swizzle is in
+// each lane's global address), int8 codes through registers, where they become
+// bf16 (exact); their scales multiply the scores and the softmax weights.  Two
+// LDS buffers, the next tile's loads in flight during this one's products, one
+// barrier a tile; a wave loads the 16 tokens of one quarter, so that it needs
+// one page.
+//
+// The maximum is only moved when a score passes it by 8 (in units of log 2):
+// weights up to 2^8 lose nothing in bf16 or fp32, and the 64 to 128
+// accumulators are rarely rescaled.
 #include "kv_attn.h"
 
 namespace w4 {
@@ -26,26 +33,27 @@ namespace w4 {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kRows = 128, kTile = 64, kThreads = 256;
+constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ v16f mfma32(uint4 a, uint4 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
                                                    __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Byte offset of 16-byte chunk `chunk` of token `t` in a K tile.
+// Swizzles: what the index of a token's 16-byte chunk is XORed with.  K is read
+// 16 rows of one chunk at a time, V 8 rows of 4 chunks; a row of 64 values is
+// half of the banks.
 template <int DP>
-__device__ __forceinline__ int k_at(int t, int chunk) {
-    const int x = DP == 64 ? (t >> 1) & 7 : t & 15;
-    return t * DP * 2 + ((chunk ^ x) << 4);
+__device__ __forceinline__ int k_swizzle(int t) {
+    return DP == 64 ? (t >> 1) & 7 : t & 15;
 }
-
-// Byte offset of chunk `chunk` (8 token places) of value d in a V^T tile.
-// Place 8 h + j of the 16 tokens of chunks 2 i, 2 i + 1 is token
-// 16 i + 8 (j / 4) + 4 h + j % 4: what lane half h holds of S^T.
-__device__ __forceinline__ int v_at(int d, int chunk) {
-    return d * kTile * 2 + ((chunk ^ ((d ^ (d >> 3) ^ (d >> 6)) & 7)) << 4);
+template <int DP>
+__device__ __forceinline__ int v_swizzle(int t) {
+    return DP == 64 ? ((t >> 1) & 3) * 2 : (t & 7) * 2;
 }
 
 // Tile index of the first tile of sequence b: the sequences' tiles lie in
@@ -69,21 +77,11 @@ __device__ __forceinline__ int64_t find_tile(const KvAttnArgs &a, int G, int64_t
     return lo;
 }
 
-// Loads of one K / V tile in registers.  Thread t has K chunks t % kCh of rows
-// t / kCh + ..., and V values (t % 16) VE ... of the tokens 4 (t / 16) ... + 3.
-template <int DP, bool INT8>
-struct Stage {
-    static constexpr int kB = INT8 ? 1 : 2;
-    static constexpr int kCh = DP * kB / 16;           // 16-byte chunks of a row
-    static constexpr int kLoads = kTile * kCh / kThreads;
-    static constexpr int kStep = kThreads / kCh;       // rows between a thread's loads
-    static constexpr int VE = DP / 16;
-    static constexpr int kW = VE * kB / 4;             // dwords of a V piece
-    u32x4 k[kLoads];
-    uint32_t v[4][kW];
-    float ks, vs;
-    int bad;  // tokens (bits 0 .. 3) of v that no row of the workgroup sees
-};
+// Sum of a packed bf16 pair and c.
+__device__ __forceinline__ float add_pair(uint32_t w, float c) {
+    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, c, false);
+}
 
 // One query row without the matrix cores, token by token, so that a token the
 // row does not see takes no part at all: for workgroups whose edge tiles hold
@@ -151,10 +149,11 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
 
 template <int DP, bool INT8, bool FP32>
 __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_prefill(KvAttnArgs a) {
-    using St = Stage<DP, INT8>;
-    constexpr int kSteps = DP / 16, kDt = DP / 32, VE = St::VE;
-    constexpr int kQ = FP32 ? 3 : 1, kP = kQ;
-    constexpr int kKBytes = kTile * DP * 2, kBuf = 2 * kKBytes;
+    constexpr int kSteps = DP / 16, kDt = DP / 32, kQ = FP32 ? 3 : 1, kP = kQ;
+    constexpr int kPitch = DP * 2, kCh = DP / 8;  // an LDS row: bytes, 16-byte chunks
+    constexpr int kVTile = kTile * kPitch, kBuf = 2 * kVTile;
+    constexpr int kCode = DP / 16;                // 16-byte chunks of a row of codes
+    constexpr int kLoads = INT8 ? DP / 64 : DP / 32;  // loads of 16 rows by a wave
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ float sks[2][kTile], svs[2][kTile];
     __shared__ int odd;  // whether a tile at an edge has values of V that are not finite
@@ -189,121 +188,124 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     const int sink_tiles = min((a.sinks + kTile - 1) / kTile, lo_tile);
     const int tiles = pos1 < 0 ? 0 : sink_tiles + pos1 / kTile + 1 - lo_tile;
     const int32_t *table = a.c.table + b * a.c.W;
-    const float scale2 = a.scale * 1.44269504088896340736f;
+
+    // scores in units of log 2 are sc times S; a scale below zero turns q's
+    // signs, one of zero clears q, so that sc > 0 and the maximum of S serves
+    const float sc = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.44269504088896340736f;
+    const uint32_t q_and = a.scale == 0.0f ? 0u : ~0u, q_xor = a.scale < 0.0f ? 0x80008000u : 0u;
 
     // q stays in registers as the B operand, but for the three terms of 256 dims
     // (192 registers beside 128 of O): those are read and split for every tile
     constexpr bool kKeep = !(FP32 && DP == 256);
     const int64_t q_at = (c0 + tok) * a.ldq + head * D + half * 8;
     uint4 q[kQ][kKeep ? kSteps : 1];
+    auto load_q = [&](int j, int to) {
+        load_query<FP32>(a.q, q_at + j * 16, on && j * 16 + half * 8 < D, q, to);
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) {
+            uint4 &w = q[u][to];
+            w = uint4{(w.x & q_and) ^ q_xor, (w.y & q_and) ^ q_xor, (w.z & q_and) ^ q_xor,
+                      (w.w & q_and) ^ q_xor};
+        }
+    };
     if constexpr (kKeep)
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-            load_query<FP32>(a.q, q_at + j * 16, on && j * 16 + half * 8 < D, q, j);
+        for (int j = 0; j < kSteps; ++j) load_q(j, j);
 
     auto tile_token = [&](int i) {
         return kTile * (i < sink_tiles ? i : i - sink_tiles + lo_tile);
     };
-    // pages of the four 16-token quarters of a tile (-1: none)
-    auto tile_pages = [&](int t0, int (&page)[4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) page[j] = kv_page(a.c, table, t0 + 16 * j);
+    // pages of the next 16 tiles, one lane for each 16 tokens
+    int base = 0, pages = -1;
+    uint64_t gone = 0;  // lanes without a page
+    auto look_up = [&](int i) {
+        const int ii = i + lane / 4;
+        base = i;
+        pages = ii < tiles ? kv_page(a.c, table, tile_token(ii) + lane % 4 * 16) : -1;
+        gone = __ballot(pages < 0);
     };
+    auto gone_of = [&](int i) { return (int)(gone >> (4 * (i - base))) & 15; };
     // whether some row does not see some token of the tile
-    auto at_edge = [&](int t0, const int (&page)[4]) {
+    auto at_edge = [&](int t0, int none) {
         return t0 + kTile - 1 > pos0 || (a.window && t0 < low1 && t0 + kTile > a.sinks) ||
-               (page[0] | page[1] | page[2] | page[3]) < 0;
+               none != 0;
     };
-    auto load = [&](St &st, int t0, const int (&page)[4]) {
-#pragma unroll
-        for (int j = 0; j < St::kLoads; ++j) {
-            const int t = tid / St::kCh + j * St::kStep, ch = tid % St::kCh;
-            // (a wave's rows of one load lie in one quarter)
-            const int qt = __builtin_amdgcn_readfirstlane(t / 16);
-            const int pg = qt == 0 ? page[0] : qt == 1 ? page[1] : qt == 2 ? page[2] : page[3];
-            const int64_t vec = kv_vector(a.c, max(pg, 0), kvh, t0 + 16 * qt) + t % 16;
-            const int d = ch * (16 / St::kB);
-            st.k[j] = *reinterpret_cast<const u32x4 *>(a.c.k + (vec * D + (d < D ? d : 0)) * St::kB);
-        }
-        const int pg = wave == 0 ? page[0] : wave == 1 ? page[1] : wave == 2 ? page[2] : page[3];
-        const int64_t vec0 = kv_vector(a.c, max(pg, 0), kvh, t0 + 16 * wave);
-        const int t = lane / 16 * 4, d = lane % 16 * VE;
-        const uint8_t *vp = a.c.v + ((vec0 + t) * D + (d < D ? d : 0)) * St::kB;
-        st.bad = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int w = 0; w < St::kW; w += St::kW < 4 ? St::kW : 4) {
-                const uint8_t *p = vp + j * D * St::kB + w * 4;
-                if constexpr (St::kW >= 4) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-                    st.v[j][w] = x.x, st.v[j][w + 1] = x.y;
-                    st.v[j][w + 2] = x.z, st.v[j][w + 3] = x.w;
-                } else if constexpr (St::kW == 2) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-                    st.v[j][0] = x.x, st.v[j][1] = x.y;
-                } else {
-                    st.v[j][0] = *reinterpret_cast<const uint32_t *>(p);
-                }
-            }
-            const int tj = t0 + 16 * wave + t + j;
-            const bool seen = tj <= pos1 && (tj >= low0 || tj < a.sinks) && pg >= 0;
-            if (!seen) st.bad |= 1 << j;
-        }
+
+    // Lane offsets of the loads: chunk (lane % chunks) of LDS row (lane / chunks)
+    // holds the token's chunk at that place XOR the row's swizzle.
+    constexpr int kRowsPer = INT8 ? 64 / kCode : 64 / kCh;  // rows of a load
+    u32x4 stage[INT8 ? 2 * kLoads : 1];
+    float ks = 0.0f, vs = 0.0f;
+    auto load = [&](int i, int buf) {
+        const int t0 = tile_token(i);
+        const int pg = __builtin_amdgcn_readlane(pages, 4 * (i - base) + wave);
+        const int64_t vec = kv_vector(a.c, max(pg, 0), kvh, t0 + 16 * wave);
         if constexpr (INT8) {
-            // lanes 0 .. 15 of a wave: the scales of its 16 tokens
-            st.ks = a.c.ks[vec0 + lane % 16];
-            st.vs = a.c.vs[vec0 + lane % 16];
+            const int ch = lane % kCode * 16;
+            const uint32_t off = lane / kCode * D + (ch < D ? ch : 0);
+            const uint8_t *kp = a.c.k + vec * D, *vp = a.c.v + vec * D;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j, kp += kRowsPer * D, vp += kRowsPer * D) {
+                stage[j] = *reinterpret_cast<const u32x4 *>(kp + off);
+                stage[kLoads + j] = *reinterpret_cast<const u32x4 *>(vp + off);
+            }
+            ks = a.c.ks[vec + lane % 16];
+            vs = a.c.vs[vec + lane % 16];
+        } else {
+            const v4i kd = buffer_desc(a.c.k + vec * D * 2, 16 * D * 2);
+            const v4i vd = buffer_desc(a.c.v + vec * D * 2, 16 * D * 2);
+            const uint32_t to = lds_addr(lds) + buf * kBuf + wave * 16 * kPitch;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int t = j * kRowsPer + lane / kCh;  // of the quarter's 16
+                const int kc = ((lane % kCh) ^ k_swizzle<DP>(t)) * 8;
+                const int vc = ((lane % kCh) ^ v_swizzle<DP>(t)) * 8;
+                dma16(kd, to + j * 1024, (t * D + (kc < D ? kc : 0)) * 2, 0);
+                dma16(vd, to + kVTile + j * 1024, (t * D + (vc < D ? vc : 0)) * 2, 0);
+            }
         }
     };
-    auto store = [&](St &st, int buf, bool edge) {
-        uint8_t *kb = lds + buf * kBuf, *vb = kb + kKBytes;
-#pragma unroll
-        for (int j = 0; j < St::kLoads; ++j) {
-            const int t = tid / St::kCh + j * St::kStep, ch = tid % St::kCh;
-            if constexpr (INT8) {
-                *reinterpret_cast<uint4 *>(kb + k_at<DP>(t, 2 * ch)) = codes8(__builtin_bit_cast(uint4, st.k[j]), 0);
-                *reinterpret_cast<uint4 *>(kb + k_at<DP>(t, 2 * ch + 1)) = codes8(__builtin_bit_cast(uint4, st.k[j]), 1);
-            } else {
-                *reinterpret_cast<u32x4 *>(kb + k_at<DP>(t, ch)) = st.k[j];
-            }
-        }
-        if (edge) {
-            // values that no row sees may be anything: clear them; those that
-            // some rows see and others do not must be finite for the product
-            // with a weight of zero: note where they are not
-            bool inf = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int w = 0; w < St::kW; ++w) {
-                    if (st.bad >> j & 1) st.v[j][w] = 0;
-                    if constexpr (!INT8)
-                        inf |= (st.v[j][w] & 0x7F80u) == 0x7F80u ||
-                               (st.v[j][w] & 0x7F800000u) == 0x7F800000u;
-                }
-            if (inf) odd = 1;
-        }
-        const int t4 = lane / 16;  // tokens 4 t4 .. + 3 of the wave's 16
-        const int chunk = wave * 2 + t4 % 2, sub = t4 / 2 * 8;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            uint2 x;
-            if constexpr (INT8) {
-                const int w = e / 4, s = e % 4 * 8;
-                x.x = code_pair((int8_t)(st.v[0][w] >> s), (int8_t)(st.v[1][w] >> s));
-                x.y = code_pair((int8_t)(st.v[2][w] >> s), (int8_t)(st.v[3][w] >> s));
-            } else {
-                const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
-                x.x = __builtin_amdgcn_perm(st.v[1][e / 2], st.v[0][e / 2], sel);
-                x.y = __builtin_amdgcn_perm(st.v[3][e / 2], st.v[2][e / 2], sel);
-            }
-            *reinterpret_cast<uint2 *>(vb + v_at(lane % 16 * VE + e, chunk) + sub) = x;
-        }
+    // The tile's last steps before its barrier, by the wave that loaded a quarter.
+    auto finish = [&](int i, int buf, bool edge) {
+        uint8_t *kb = lds + buf * kBuf + wave * 16 * kPitch, *vb = kb + kVTile;
         if constexpr (INT8) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int t = j * kRowsPer + lane / kCode, ch = lane % kCode * 2;
+                const uint4 k = __builtin_bit_cast(uint4, stage[j]);
+                const uint4 v = __builtin_bit_cast(uint4, stage[kLoads + j]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    *reinterpret_cast<uint4 *>(
+                        kb + t * kPitch + (((ch + x) ^ k_swizzle<DP>(t)) << 4)) = codes8(k, x);
+                    *reinterpret_cast<uint4 *>(
+                        vb + t * kPitch + (((ch + x) ^ v_swizzle<DP>(t)) << 4)) = codes8(v, x);
+                }
+            }
             if (lane < 16) {
-                sks[buf][wave * 16 + lane] = st.ks;
-                svs[buf][wave * 16 + lane] = st.vs;
+                sks[buf][wave * 16 + lane] = ks;
+                svs[buf][wave * 16 + lane] = vs;
+            }
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (edge) {
+                // V of tokens that no row sees may be anything: clear it; what some
+                // rows see and others do not must be finite for the product with a
+                // weight of zero: note where it is not
+                const int t = tile_token(i) + 16 * wave + lane / 4;
+                const bool seen = t <= pos1 && (t >= low0 || t < a.sinks) &&
+                                  !(gone_of(i) >> wave & 1);
+                bool inf = false;
+#pragma unroll 1
+                for (int ch = lane % 4; ch < kCh; ch += 4) {
+                    u32x4 *p = reinterpret_cast<u32x4 *>(vb + lane / 4 * kPitch + ch * 16);
+                    const u32x4 x = *p;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        inf |= (x[w] & 0x7F80u) == 0x7F80u || (x[w] & 0x7F800000u) == 0x7F800000u;
+                    if (!seen) *p = u32x4{0, 0, 0, 0};
+                }
+                if (seen && inf) odd = 1;
             }
         }
     };
@@ -312,54 +314,60 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     __syncthreads();
     v16f o[kDt] = {};
     float m = -INFINITY, l = 0.0f;
-    St st;
-    int page[4], next[4] = {};
     bool edge = false;
+    int none = 0;
     if (tiles > 0) {
-        const int t0 = tile_token(0);
-        tile_pages(t0, page);
-        edge = at_edge(t0, page);
-        load(st, t0, page);
-        store(st, 0, edge);
+        look_up(0);
+        none = gone_of(0);
+        edge = at_edge(tile_token(0), none);
+        load(0, 0);
+        finish(0, 0, edge);
     }
     __syncthreads();
+    // lane addresses in a tile: K's chunk `half` of row col, V's chunk of the
+    // first rows of a transposing read (see the top)
+    const int k_lane = col * kPitch, k_x = (half ^ k_swizzle<DP>(col)) << 4;
+    const int v_row = half * 4 + lane % 16 / 4;
+    const int v_lane = v_row * kPitch + (lane & 1) * 8;
+    const int v_x = ((lane / 16 % 2 * 2 + lane % 4 / 2) ^ v_swizzle<DP>(v_row)) << 4;
     for (int i = 0; i < tiles; ++i) {
         const int buf = i & 1;
         const int t0 = tile_token(i);
+        const bool more = i + 1 < tiles;
         bool next_edge = false;
-        if (i + 1 < tiles) {
-            const int t1 = tile_token(i + 1);
-            tile_pages(t1, next);
-            next_edge = at_edge(t1, next);
-            load(st, t1, next);
+        int next_none = 0;
+        if (more) {
+            if (i + 1 - base >= 16) look_up(i + 1);
+            next_none = gone_of(i + 1);
+            next_edge = at_edge(tile_token(i + 1), next_none);
+            load(i + 1, buf ^ 1);
         }
-        const uint8_t *kb = lds + buf * kBuf, *vb = kb + kKBytes;
+        const uint8_t *kb = lds + buf * kBuf + k_lane;
+        const uint32_t vb = lds_addr(lds) + buf * kBuf + kVTile + v_lane;
         v16f s[2] = {};
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            if constexpr (!kKeep)
-                load_query<FP32>(a.q, q_at + j * 16, on && j * 16 + half * 8 < D, q, 0);
+            if constexpr (!kKeep) load_q(j, 0);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint4 kk = *reinterpret_cast<const uint4 *>(
-                    kb + k_at<DP>(t * 32 + col, j * 2 + half));
+                const uint4 kk =
+                    *reinterpret_cast<const uint4 *>(kb + t * 32 * kPitch + (k_x ^ (j * 32)));
 #pragma unroll
                 for (int u = kQ - 1; u >= 0; --u) s[t] = mfma32(kk, q[u][kKeep ? j : 0], s[t]);
             }
         }
-        // scores in units of log 2; token of register r: 32 t + 8 (r / 4) + 4 half + r % 4
+        // token of register r: 32 t + 8 (r / 4) + 4 half + r % 4
+        if constexpr (INT8) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                float4 ks = {1.0f, 1.0f, 1.0f, 1.0f};
-                if constexpr (INT8)
-                    ks = *reinterpret_cast<const float4 *>(&sks[buf][32 * t + 8 * r4 + 4 * half]);
-                s[t][4 * r4] *= INT8 ? scale2 * ks.x : scale2;
-                s[t][4 * r4 + 1] *= INT8 ? scale2 * ks.y : scale2;
-                s[t][4 * r4 + 2] *= INT8 ? scale2 * ks.z : scale2;
-                s[t][4 * r4 + 3] *= INT8 ? scale2 * ks.w : scale2;
-            }
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const v4f x =
+                        *reinterpret_cast<const v4f *>(&sks[buf][32 * t + 8 * r4 + 4 * half]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][4 * r4 + e] *= x[e];
+                }
+        }
         if (edge) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -367,8 +375,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 for (int r = 0; r < 16; ++r) {
                     const int tj = t0 + 32 * t + 8 * (r / 4) + 4 * half + r % 4;
                     const bool see = tj <= pos && (tj >= low || tj < a.sinks) &&
-                                     page[2 * t + r / 8] >= 0;
-                    if (!see) s[t][r] = -INFINITY;
+                                     !(none >> (2 * t + r / 8) & 1);
+                    s[t][r] = see ? s[t][r] : -INFINITY;
                 }
         }
         float mt = s[0][0];
@@ -376,8 +384,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[t][r]);
-        mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
-        if (__any(mt > m)) {
+        mt = fmaxf(mt, __shfl_xor(mt, 32, kWave)) * sc;
+        if (__any(mt > m + kSlack)) {
             const float mn = fmaxf(m, mt);
             const float alpha = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
@@ -387,48 +395,54 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
         }
-        const float mu = m == -INFINITY ? 0.0f : m;
-        uint4 p[kP][4];
+        const float mu = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {  // 16 tokens: registers 8 (i4 % 2) ... of half i4 / 2
             float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float e = __builtin_amdgcn_exp2f(s[i4 / 2][8 * (i4 % 2) + j] - mu);
-                l += e;
-                f[j] = e;
+            for (int j = 0; j < 8; ++j)
+                f[j] = __builtin_amdgcn_exp2f(
+                    __builtin_fmaf(s[i4 / 2][8 * (i4 % 2) + j], sc, mu));
+            if constexpr (INT8 || FP32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) l += f[j];
             }
             if constexpr (INT8) {
 #pragma unroll
                 for (int j4 = 0; j4 < 2; ++j4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
+                    const v4f x = *reinterpret_cast<const v4f *>(
                         &svs[buf][16 * i4 + 8 * j4 + 4 * half]);
                     // (a weight of zero stays zero whatever an unseen token's scale is)
-                    f[4 * j4] = f[4 * j4] == 0.0f ? 0.0f : f[4 * j4] * v.x;
-                    f[4 * j4 + 1] = f[4 * j4 + 1] == 0.0f ? 0.0f : f[4 * j4 + 1] * v.y;
-                    f[4 * j4 + 2] = f[4 * j4 + 2] == 0.0f ? 0.0f : f[4 * j4 + 2] * v.z;
-                    f[4 * j4 + 3] = f[4 * j4 + 3] == 0.0f ? 0.0f : f[4 * j4 + 3] * v.w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[4 * j4 + e] = f[4 * j4 + e] == 0.0f ? 0.0f : f[4 * j4 + e] * x[e];
                 }
             }
-            uint4 w[kP];
-            split_bf16<kP>(f, w);
-#pragma unroll
-            for (int u = 0; u < kP; ++u) p[u][i4] = w[u];
-        }
-#pragma unroll
-        for (int d = 0; d < kDt; ++d)
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-                const uint4 vv = *reinterpret_cast<const uint4 *>(
-                    vb + v_at(d * 32 + col, i4 * 2 + half));
-#pragma unroll
-                for (int u = kP - 1; u >= 0; --u) o[d] = mfma32(vv, p[u][i4], o[d]);
+            uint4 p[kP];
+            split_bf16<kP>(f, p);
+            if constexpr (!INT8 && !FP32) {
+                // (the sum of the rounded weights, as the product takes them)
+                l = add_pair(p[0].x, l);
+                l = add_pair(p[0].y, l);
+                l = add_pair(p[0].z, l);
+                l = add_pair(p[0].w, l);
             }
-        if (i + 1 < tiles) store(st, buf ^ 1, next_edge);
-        edge = next_edge;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) page[j] = next[j];
-        __syncthreads();
+            for (int d = 0; d < kDt; ++d) {
+                const uint32_t at = vb + i4 * 16 * kPitch + (v_x ^ (d * 64));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
+                const s16x4 hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * kPitch));
+                const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+                const uint4 vv = {x.x, x.y, y.x, y.y};
+#pragma unroll
+                for (int u = kP - 1; u >= 0; --u) o[d] = mfma32(vv, p[u], o[d]);
+            }
+        }
+        if (more) finish(i + 1, buf ^ 1, next_edge);
+        edge = next_edge;
+        none = next_none;
+        lds_barrier();
     }
 
     if (!INT8 && odd) {
@@ -444,15 +458,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     // O^T -> rows through LDS (the tiles are done), then whole rows to memory
     l += __shfl_xor(l, 32, kWave);
     const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    constexpr int kE = FP32 ? 4 : 2, kPitch = DP * kE + 16;
-    uint8_t *ob = lds + wave * 32 * kPitch;
+    constexpr int kE = FP32 ? 4 : 2, kOut = DP * kE + 16;
+    uint8_t *ob = lds + wave * 32 * kOut;
 #pragma unroll
     for (int d = 0; d < kDt; ++d)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const float4 y = {o[d][4 * r4] * inv, o[d][4 * r4 + 1] * inv, o[d][4 * r4 + 2] * inv,
                               o[d][4 * r4 + 3] * inv};
-            uint8_t *to = ob + col * kPitch + (d * 32 + 8 * r4 + 4 * half) * kE;
+            uint8_t *to = ob + col * kOut + (d * 32 + 8 * r4 + 4 * half) * kE;
             if constexpr (FP32)
                 *reinterpret_cast<float4 *>(to) = y;
             else
@@ -467,7 +481,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         const int64_t tk = rr / G;
         const int64_t to = ((c0 + tk) * a.hq + kvh * G + (rr - tk * G)) * D * kE + x * 16;
         *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.out) + to) =
-            *reinterpret_cast<const uint4 *>(ob + r * kPitch + x * 16);
+            *reinterpret_cast<const uint4 *>(ob + r * kOut + x * 16);
     }
 }
 
