@@ -45,15 +45,15 @@ __device__ __forceinline__ v16f mfma32(uint4 a, uint4 b, v16f c) {
 }
 
 // Swizzles: what the index of a token's 16-byte chunk is XORed with.  K is read
-// 16 rows of one chunk at a time, V 8 rows of 4 chunks; a row of 64 values is
-// half of the banks.
+// 16 rows of one chunk at a time, V 4 rows of 4 chunks (half a transposing
+// read); a row of 64 values is half of the banks.
 template <int DP>
 __device__ __forceinline__ int k_swizzle(int t) {
     return DP == 64 ? (t >> 1) & 7 : t & 15;
 }
 template <int DP>
 __device__ __forceinline__ int v_swizzle(int t) {
-    return DP == 64 ? ((t >> 1) & 3) * 2 : (t & 7) * 2;
+    return DP == 64 ? ((t >> 1) & 1) * 4 : (t & 3) * 4;
 }
 
 // Tile index of the first tile of sequence b: the sequences' tiles lie in
@@ -344,17 +344,28 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         }
         const uint8_t *kb = lds + buf * kBuf + k_lane;
         const uint32_t vb = lds_addr(lds) + buf * kBuf + kVTile + v_lane;
+        // fragments are read kDeep steps ahead of their products
+        constexpr int kDeep = DP == 256 ? 2 : 3;
         v16f s[2] = {};
+        uint4 kf[kDeep + 1][2];
+        auto read_k = [&](int j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                kf[j % (kDeep + 1)][t] =
+                    *reinterpret_cast<const uint4 *>(kb + t * 32 * kPitch + (k_x ^ (j * 32)));
+        };
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) read_k(j);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
+            if (j + kDeep < kSteps) read_k(j + kDeep);
             if constexpr (!kKeep) load_q(j, 0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint4 kk =
-                    *reinterpret_cast<const uint4 *>(kb + t * 32 * kPitch + (k_x ^ (j * 32)));
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int u = kQ - 1; u >= 0; --u) s[t] = mfma32(kk, q[u][kKeep ? j : 0], s[t]);
-            }
+                for (int u = kQ - 1; u >= 0; --u)
+                    s[t] = mfma32(kf[j % (kDeep + 1)][t], q[u][kKeep ? j : 0], s[t]);
         }
         // token of register r: 32 t + 8 (r / 4) + 4 half + r % 4
         if constexpr (INT8) {
@@ -374,11 +385,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int tj = t0 + 32 * t + 8 * (r / 4) + 4 * half + r % 4;
-                    const bool see = tj <= pos && (tj >= low || tj < a.sinks) &&
+                    const bool see = (tj <= pos) & ((tj >= low) | (tj < a.sinks)) &
                                      !(none >> (2 * t + r / 8) & 1);
                     s[t][r] = see ? s[t][r] : -INFINITY;
                 }
         }
+        // (the other wave of the SIMD is in its products by then: apart in phase, the
+        // two share the matrix cores and the VALU better)
+        __builtin_amdgcn_s_setprio(1);
         float mt = s[0][0];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -396,6 +410,19 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
         }
         const float mu = m == -INFINITY ? 0.0f : -m;
+        constexpr int kAheadV = 3;
+        constexpr int kVMask = 0x2 | 0x4 | 0x400;  // VALU, SALU and transcendentals may pass
+        uint4 vf[kAheadV + 1];
+        auto read_v = [&](int n) {
+            const uint32_t at = vb + n / kDt * 16 * kPitch + (v_x ^ (n % kDt * 64));
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
+            const s16x4 hi =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * kPitch));
+            const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+            vf[n % (kAheadV + 1)] = uint4{x.x, x.y, y.x, y.y};
+        };
+#pragma unroll
+        for (int n = 0; n < kAheadV; ++n) read_v(n);
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {  // 16 tokens: registers 8 (i4 % 2) ... of half i4 / 2
             float f[8];
@@ -429,16 +456,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
             }
 #pragma unroll
             for (int d = 0; d < kDt; ++d) {
-                const uint32_t at = vb + i4 * 16 * kPitch + (v_x ^ (d * 64));
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
-                const s16x4 hi =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * kPitch));
-                const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
-                const uint4 vv = {x.x, x.y, y.x, y.y};
+                const int n = i4 * kDt + d;
+                if (n + kAheadV < 4 * kDt) read_v(n + kAheadV);
+                __builtin_amdgcn_sched_barrier(kVMask);
 #pragma unroll
-                for (int u = kP - 1; u >= 0; --u) o[d] = mfma32(vv, p[u], o[d]);
+                for (int u = kP - 1; u >= 0; --u)
+                    o[d] = mfma32(vf[n % (kAheadV + 1)], p[u], o[d]);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         if (more) finish(i + 1, buf ^ 1, next_edge);
         edge = next_edge;
         none = next_none;
