@@ -284,7 +284,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
             }
             if (lane < 16) {
                 sks[buf][wave * 16 + lane] = ks;
-                svs[buf][wave * 16 + lane] = vs;
+                // (finite, so that an unseen token's weight of zero stays zero)
+                svs[buf][wave * 16 + lane] = fminf(vs, 3.0e38f);
             }
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -344,8 +345,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         }
         const uint8_t *kb = lds + buf * kBuf + k_lane;
         const uint32_t vb = lds_addr(lds) + buf * kBuf + kVTile + v_lane;
-        // fragments are read kDeep steps ahead of their products
-        constexpr int kDeep = DP == 256 ? 2 : 3;
+        // fragments are read a step ahead of their products (more measured the same)
+        constexpr int kDeep = 1;
         v16f s[2] = {};
         uint4 kf[kDeep + 1][2];
         auto read_k = [&](int j) {
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
         }
         const float mu = m == -INFINITY ? 0.0f : -m;
-        constexpr int kAheadV = 3;
+        constexpr int kAheadV = 1;
         constexpr int kVMask = 0x2 | 0x4 | 0x400;  // VALU, SALU and transcendentals may pass
         uint4 vf[kAheadV + 1];
         auto read_v = [&](int n) {
@@ -439,10 +440,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 for (int j4 = 0; j4 < 2; ++j4) {
                     const v4f x = *reinterpret_cast<const v4f *>(
                         &svs[buf][16 * i4 + 8 * j4 + 4 * half]);
-                    // (a weight of zero stays zero whatever an unseen token's scale is)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        f[4 * j4 + e] = f[4 * j4 + e] == 0.0f ? 0.0f : f[4 * j4 + e] * x[e];
+                    for (int e = 0; e < 4; ++e) f[4 * j4 + e] *= x[e];
                 }
             }
             uint4 p[kP];
