@@ -381,7 +381,9 @@ int w4a8_linear_prepacked(const float *X, int64_t M, int64_t K, int64_t N,
  * 16-byte pieces in both types (one page is then a contiguous run of every
  * head's tokens).  1 <= heads <= 65535, layers * pages * heads * page_size *
  * head_dim <= 2^46, pages < 2^31.  A call takes up to 2^23 rows, forks, slots
- * or page pairs and up to 2^26 token-head vectors (else W4_ERR_SHAPE).  k, v and the scales are 16-byte aligned.
+ * or page pairs, up to 2^26 token-head vectors and, for attention, up to 2^28
+ * (token, query head) and 2^22 (sequence, query head) pairs (else
+ * W4_ERR_SHAPE).  k, v and the scales are 16-byte aligned.
  * Values in device memory cannot be checked on the host; the kernels read and
  * write nothing outside the arrays whatever the tables, lengths and offsets
  * hold: a table entry outside [0, pages) is no page, a token without a page is

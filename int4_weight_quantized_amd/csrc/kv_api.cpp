@@ -19,6 +19,8 @@ constexpr int64_t kMaxValues = (int64_t)1 << 46;  // values of K in a cache
 // each at most) and token-head vectors (32 threads each at most)
 constexpr int64_t kMaxRows = (int64_t)1 << 23;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // of one sequence
+constexpr int64_t kMaxQueries = (int64_t)1 << 28;  // (token, query head) pairs of a call
+constexpr int64_t kMaxPairs = (int64_t)1 << 22;    // (sequence, query head) pairs
 constexpr int64_t kMaxVectors = (int64_t)1 << 26;
 
 // a * b, or kMaxValues + 1 where it is more (a, b >= 1)
@@ -124,7 +126,8 @@ int attention(const char *path, const kv_cache *c, int64_t layer, const void *q,
     if (x_dtype != KV_X_BF16 && x_dtype != KV_X_FP32) return W4_ERR_ARG;
     if (layer < 0 || layer >= c->layers || window < 0 || sinks < 0 || !std::isfinite(scale))
         return W4_ERR_ARG;
-    if (T < 1 || T > kMaxRows || hq < 1 || hq % c->heads != 0 || hq > 65535)
+    if (T < 1 || T > kMaxRows || hq < 1 || hq % c->heads != 0 || hq > 65535 ||
+        T > kMaxQueries / hq || B > kMaxPairs / hq)
         return W4_ERR_SHAPE;
     if (ldq < hq * c->head_dim || ldq > kMaxValues / T) return W4_ERR_SHAPE;
     const size_t esize = x_dtype == KV_X_FP32 ? 4 : 2;
@@ -189,7 +192,7 @@ size_t kv_attention_workspace_bytes(int64_t rows, int64_t B, int64_t q_heads, in
                                     int64_t head_dim) {
     if (rows < 1 || B < 1 || q_heads < 1 || heads < 1 || head_dim < 16 || head_dim > 256 ||
         head_dim % 16 != 0 || q_heads % heads != 0 || q_heads > 65535 ||
-        rows > kMaxRows || B > kMaxInt)
+        rows > kMaxRows || rows > kMaxQueries / q_heads || B > kMaxPairs / q_heads)
         return 0;
     return w4::kv_attn_ws_bytes(rows, B, q_heads, heads, head_dim);
 }

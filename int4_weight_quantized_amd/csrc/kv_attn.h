@@ -9,6 +9,7 @@ namespace w4 {
 
 size_t kv_decode_ws_bytes(int64_t hq, int64_t heads, int64_t D);
 hipError_t launch_kv_decode(const KvAttnArgs &a, hipStream_t st);
+size_t kv_prefill_ws_bytes(int64_t T, int64_t B, int64_t hq, int64_t heads, int64_t D);
 hipError_t launch_kv_prefill(const KvAttnArgs &a, hipStream_t st);
 
 // Two int8 codes as a bf16 pair: 8 bits are exact in bf16, so the upper halves
@@ -88,6 +89,21 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, float4 y, float
 constexpr int64_t kMaxLength = (int64_t)1 << 30;
 __device__ __forceinline__ int kv_length(const KvAttnArgs &a, int64_t b) {
     return min(max(a.lens[b], 0), (int)min(a.c.W << a.c.shift, kMaxLength));
+}
+
+// (m, l, y) += another part (mk, lk, z) of the same row.
+__device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk, float lk,
+                                         float4 z) {
+    if (mk == -INFINITY) return;
+    const float mn = fmaxf(m, mk);
+    const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+    const float fb = __builtin_amdgcn_exp2f(mk - mn);
+    m = mn;
+    l = l * fa + lk * fb;
+    y.x = y.x * fa + z.x * fb;
+    y.y = y.y * fa + z.y * fb;
+    y.z = y.z * fa + z.z * fb;
+    y.w = y.w * fa + z.w * fb;
 }
 
 // First vector (page, head, slot) of the 16 tokens from `token` on.

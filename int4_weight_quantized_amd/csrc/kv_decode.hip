@@ -555,21 +555,6 @@ __global__ __launch_bounds__(
     if (SPLIT && threadIdx.x == 0) reinterpret_cast<KvSplitPair *>(a.ws)[blockIdx.x] = mark;
 }
 
-// (m, l, y) += another part (mk, lk, z) of the same row.
-__device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk, float lk,
-                                         float4 z) {
-    if (mk == -INFINITY) return;
-    const float mn = fmaxf(m, mk);
-    const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
-    const float fb = __builtin_amdgcn_exp2f(mk - mn);
-    m = mn;
-    l = l * fa + lk * fb;
-    y.x = y.x * fa + z.x * fb;
-    y.y = y.y * fa + z.y * fb;
-    y.z = y.z * fa + z.z * fb;
-    y.w = y.w * fa + z.w * fb;
-}
-
 // Joins the parts of the pair that workgroup blockIdx.x of the split kernel
 // started and others went on with, in the workgroups' order.
 template <int DP, bool FP32>

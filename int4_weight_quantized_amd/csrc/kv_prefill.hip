@@ -83,14 +83,25 @@ __device__ __forceinline__ float add_pair(uint32_t w, float c) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, c, false);
 }
 
+// Where a row's result goes: to its place in the output, or, where the tiles of a
+// row go to several workgroups, as the unnormalized part of this one.
+struct RowOut {
+    int64_t row;   // token * q_heads + head
+    int part, parts;
+    __device__ float *sums(const KvAttnArgs &a) const {  // D sums, m, l
+        return reinterpret_cast<float *>(a.ws) + (row * parts + part) * (a.c.D + 4);
+    }
+};
+
 // One query row without the matrix cores, token by token, so that a token the
 // row does not see takes no part at all: for workgroups whose edge tiles hold
 // infinities or NaN in V (the products of a tile would carry them to every
-// row as 0 * inf).  bf16 cache; the whole workgroup, `buf` 516 floats of LDS.
-template <bool FP32>
+// row as 0 * inf).  bf16 cache; the whole workgroup, `buf` 516 floats of LDS;
+// tile_token(i) is the first token of tile i, i from i0 to i1 - 1.
+template <bool FP32, class F>
 __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t token, int h, int kvh,
-                          int pos, float *buf) {
-    float *q = buf, *p = buf + 256, *red = buf + 512;
+                          int pos, F tile_token, int i0, int i1, RowOut out, float *buf) {
+    float *q = buf, *p = buf + 256;
     const int tid = threadIdx.x, D = a.c.D;
     const int low = a.window ? pos - a.window + 1 : 0;
     __syncthreads();
@@ -106,49 +117,53 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
         return pg < 0 ? (int64_t)-1 : kv_vector(a.c, pg, kvh, t);
     };
     float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int t0 = 0; t0 <= pos; t0 += 256) {
-        if (t0 + 256 <= low && t0 >= a.sinks) continue;
+    for (int i = i0; i < i1; ++i) {
         __syncthreads();
-        const int t = t0 + tid;
-        const bool see = t <= pos && (t >= low || t < a.sinks);
-        const int64_t vec = see ? vector(t) : -1;
-        float s = -INFINITY;
-        if (vec >= 0) {
-            float x = 0.0f;
-            for (int d = 0; d < D; ++d) x = __builtin_fmaf(q[d], bf16_lo(ck[vec * D + d]), x);
-            s = x * a.scale;
+        const int t0 = tile_token(i), t = t0 + tid;
+        if (tid < kTile) {
+            const bool see = t <= pos && (t >= low || t < a.sinks);
+            const int64_t vec = see ? vector(t) : -1;
+            float s = -INFINITY;
+            if (vec >= 0) {
+                float x = 0.0f;
+                for (int d = 0; d < D; ++d) x = __builtin_fmaf(q[d], bf16_lo(ck[vec * D + d]), x);
+                s = x * a.scale * 1.44269504088896340736f;
+            }
+            const float mn = fmaxf(m, wave_max(s));
+            p[tid] = vec >= 0 ? __builtin_amdgcn_exp2f(s - mn) : -1.0f;  // (-1: not seen)
+            if (tid == 0) p[kTile] = mn;
         }
-        const float mx = wave_max(s);
-        if (tid % kWave == 0) red[tid / kWave] = mx;
         __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float alpha = mn == -INFINITY ? 1.0f : expf(m - mn);
-        p[tid] = vec >= 0 ? expf(s - mn) : -1.0f;  // (-1: not seen)
-        __syncthreads();
+        const float mn = p[kTile];
+        const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
         m = mn;
         l *= alpha;
         o *= alpha;
-        for (int j = 0; j < 256; ++j) {
+        for (int j = 0; j < kTile; ++j) {
             if (p[j] < 0.0f) continue;
             l += p[j];
             const int64_t vj = vector(t0 + j);
             if (tid < D) o = __builtin_fmaf(p[j], bf16_lo(cv[vj * D + tid]), o);
         }
     }
-    if (tid < D) {
+    if (out.parts > 1) {
+        float *to = out.sums(a);
+        if (tid < D) to[tid] = o;
+        if (tid == 0) to[D] = m, to[D + 1] = l;
+    } else if (tid < D) {
         const float y = l == 0.0f ? 0.0f : o / l;
-        const int64_t at = (token * a.hq + h) * D + tid;
         if constexpr (FP32)
-            reinterpret_cast<float *>(a.out)[at] = y;
+            reinterpret_cast<float *>(a.out)[out.row * D + tid] = y;
         else
-            reinterpret_cast<__bf16 *>(a.out)[at] = (__bf16)y;
+            reinterpret_cast<__bf16 *>(a.out)[out.row * D + tid] = (__bf16)y;
     }
 }
 
 }  // namespace
 
 template <int DP, bool INT8, bool FP32>
-__global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_prefill(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_prefill(KvAttnArgs a,
+                                                                                          int parts) {
     constexpr int kSteps = DP / 16, kDt = DP / 32, kQ = FP32 ? 3 : 1, kP = kQ;
     constexpr int kPitch = DP * 2, kCh = DP / 8;  // an LDS row: bytes, 16-byte chunks
     constexpr int kVTile = kTile * kPitch, kBuf = 2 * kVTile;
@@ -161,7 +176,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int D = a.c.D, G = a.hq / a.c.heads;
-    const int kvh = (int)(blockIdx.x % a.c.heads);
+    const int kvh = (int)(blockIdx.x % a.c.heads), part = blockIdx.y;
     const int64_t idx = (int64_t)gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads;
     const int64_t b = find_tile(a, G, idx);
     const int64_t c0 = a.cu[b];
@@ -188,6 +203,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     const int sink_tiles = min((a.sinks + kTile - 1) / kTile, lo_tile);
     const int tiles = pos1 < 0 ? 0 : sink_tiles + pos1 / kTile + 1 - lo_tile;
     const int32_t *table = a.c.table + b * a.c.W;
+    // this workgroup's share of the tiles
+    const int i0 = (int)((int64_t)tiles * part / parts);
+    const int i1 = (int)((int64_t)tiles * (part + 1) / parts);
 
     // scores in units of log 2 are sc times S; a scale below zero turns q's
     // signs, one of zero clears q, so that sc > 0 and the maximum of S serves
@@ -221,7 +239,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     auto look_up = [&](int i) {
         const int ii = i + lane / 4;
         base = i;
-        pages = ii < tiles ? kv_page(a.c, table, tile_token(ii) + lane % 4 * 16) : -1;
+        pages = ii < i1 ? kv_page(a.c, table, tile_token(ii) + lane % 4 * 16) : -1;
         gone = __ballot(pages < 0);
     };
     auto gone_of = [&](int i) { return (int)(gone >> (4 * (i - base))) & 15; };
@@ -317,12 +335,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     float m = -INFINITY, l = 0.0f;
     bool edge = false;
     int none = 0;
-    if (tiles > 0) {
-        look_up(0);
-        none = gone_of(0);
-        edge = at_edge(tile_token(0), none);
-        load(0, 0);
-        finish(0, 0, edge);
+    if (i0 < i1) {
+        look_up(i0);
+        none = gone_of(i0);
+        edge = at_edge(tile_token(i0), none);
+        load(i0, i0 & 1);
+        finish(i0, i0 & 1, edge);
     }
     __syncthreads();
     // lane addresses in a tile: K's chunk `half` of row col, V's chunk of the
@@ -331,10 +349,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     const int v_row = half * 4 + lane % 16 / 4;
     const int v_lane = v_row * kPitch + (lane & 1) * 8;
     const int v_x = ((lane / 16 % 2 * 2 + lane % 4 / 2) ^ v_swizzle<DP>(v_row)) << 4;
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = i0; i < i1; ++i) {
         const int buf = i & 1;
         const int t0 = tile_token(i);
-        const bool more = i + 1 < tiles;
+        const bool more = i + 1 < i1;
         bool next_edge = false;
         int next_none = 0;
         if (more) {
@@ -474,14 +492,31 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         for (int i = 0; i < rows; ++i) {
             const int64_t rr = row0 + i;
             const int tk = (int)(rr / G), h = kvh * G + (int)(rr - (int64_t)tk * G);
-            plain_row<FP32>(a, table, c0 + tk, h, kvh, len - (int)nq + tk,
+            plain_row<FP32>(a, table, c0 + tk, h, kvh, len - (int)nq + tk, tile_token, i0, i1,
+                            RowOut{(c0 + tk) * a.hq + h, part, parts},
                             reinterpret_cast<float *>(lds));
         }
         return;
     }
 
-    // O^T -> rows through LDS (the tiles are done), then whole rows to memory
     l += __shfl_xor(l, 32, kWave);
+    if (parts > 1) {
+        if (!on) return;
+        float *to = RowOut{(c0 + tok) * a.hq + head, part, parts}.sums(a);
+#pragma unroll
+        for (int d = 0; d < kDt; ++d)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const int at = d * 32 + 8 * r4 + 4 * half;
+                if (at < D)
+                    *reinterpret_cast<float4 *>(to + at) = float4{
+                        o[d][4 * r4], o[d][4 * r4 + 1], o[d][4 * r4 + 2], o[d][4 * r4 + 3]};
+            }
+        if (half == 0) to[D] = m, to[D + 1] = l;
+        return;
+    }
+
+    // O^T -> rows through LDS (the tiles are done), then whole rows to memory
     const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
     constexpr int kE = FP32 ? 4 : 2, kOut = DP * kE + 16;
     uint8_t *ob = lds + wave * 32 * kOut;
@@ -510,16 +545,54 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     }
 }
 
+// Joins the parts of every row, in their order: D / 4 lanes of a workgroup have a
+// row, four values each.
+template <bool FP32>
+__global__ __launch_bounds__(256) void k_kv_prefill_join(KvAttnArgs a, int parts) {
+    const int D = a.c.D, lanes = D / 4, rows = 256 / lanes;
+    const int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / lanes;
+    if (threadIdx.x >= rows * lanes || row >= a.T * a.hq) return;
+    const int d = threadIdx.x % lanes * 4;
+    float m = -INFINITY, l = 0.0f;
+    float4 y = {};
+    for (int i = 0; i < parts; ++i) {
+        const float *p = RowOut{row, i, parts}.sums(a);
+        add_part(m, l, y, p[D], p[D + 1], *reinterpret_cast<const float4 *>(p + d));
+    }
+    store_out<FP32>(a.out, row * D + d, y, l);
+}
+
 namespace {
+
+// Workgroups of a call for each part: tiles of 128 rows that its tokens can make.
+int64_t row_tiles(int64_t T, int64_t B, int64_t G) { return T * G / kRows + B; }
+
+// Few workgroups leave the chip idle and run through their tokens one tile after
+// another: their tiles are then split over up to 16 parts, as many as two
+// workgroups a CU take, and joined by a second launch (12 workgroups over 16 tiles,
+// fp32 heads of 64: 36 us in one part).
+int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
+    const int64_t groups = row_tiles(T, B, hq / heads) * heads;
+    return std::min<int64_t>(std::max<int64_t>(512 / groups, 1), 16);
+}
 
 template <int DP, bool INT8, bool FP32>
 hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
-    const int G = a.hq / a.c.heads;
-    const int64_t tiles = a.T * G / kRows + a.B;
+    const int64_t groups = row_tiles(a.T, a.B, a.hq / a.c.heads) * a.c.heads;
+    // tiles of the longest sequence that the table can hold and the window shows
+    int64_t most = a.c.W << a.c.shift;
+    if (a.window) most = std::min<int64_t>(most, (int64_t)a.window + a.sinks + kRows + 2 * kTile);
+    const int parts = (int)std::min(most_parts(a.T, a.B, a.hq, a.c.heads), (most + kTile - 1) / kTile);
     const size_t tile_bytes = 2 * 2 * kTile * DP * 2;
     const size_t out_bytes = kRows * (DP * (FP32 ? 4 : 2) + 16);
-    hipLaunchKernelGGL((k_kv_prefill<DP, INT8, FP32>), dim3((unsigned)(tiles * a.c.heads)),
-                       dim3(kThreads), std::max(tile_bytes, out_bytes), st, a);
+    hipLaunchKernelGGL((k_kv_prefill<DP, INT8, FP32>), dim3((unsigned)groups, parts),
+                       dim3(kThreads), std::max(tile_bytes, out_bytes), st, a, parts);
+    if (parts > 1) {
+        const int rows = 256 / (a.c.D / 4);
+        hipLaunchKernelGGL(k_kv_prefill_join<FP32>,
+                           dim3((unsigned)((a.T * a.hq + rows - 1) / rows)), dim3(256), 0, st, a,
+                           parts);
+    }
     return hipGetLastError();
 }
 
@@ -530,6 +603,11 @@ hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
 }
 
 }  // namespace
+
+size_t kv_prefill_ws_bytes(int64_t T, int64_t B, int64_t hq, int64_t heads, int64_t D) {
+    const int64_t parts = most_parts(T, B, hq, heads);
+    return parts > 1 ? (size_t)(T * hq * parts * (D + 4) * 4) : 0;
+}
 
 hipError_t launch_kv_prefill(const KvAttnArgs &a, hipStream_t st) {
     return a.c.D <= 64 ? launch_types<64>(a, st)
