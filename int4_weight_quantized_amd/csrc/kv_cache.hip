@@ -82,12 +82,16 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
                                                    const void *v, int64_t ldk, int64_t ldv,
                                                    bool vec) {
     const bool isv = blockIdx.y != 0;
-    const KvPlace p = kv_place<LPV>(c, r);
     const int d = threadIdx.x % LPV * 8;
-    const bool on = p.vec >= 0 && d < c.D;
+    const int64_t i = (int64_t)blockIdx.x * (256 / LPV) + threadIdx.x / LPV;
     float f[8] = {};
-    if (on)
-        load8<FP32>(isv ? v : k, p.token * (isv ? ldv : ldk) + (int64_t)p.head * c.D + d, vec, f);
+    if (i < r.T * c.heads && d < c.D) {  // (in flight during the search for the place)
+        const int64_t token = i / c.heads;
+        load8<FP32>(isv ? v : k, token * (isv ? ldv : ldk) + (i - token * c.heads) * c.D + d, vec,
+                    f);
+    }
+    const KvPlace p = kv_place<LPV>(c, r);
+    const bool on = p.vec >= 0 && d < c.D;
     uint8_t *pool = isv ? c.v : c.k;
     if constexpr (INT8) {
         float m = 0.0f;
@@ -105,12 +109,9 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
         if (d == 0) (isv ? c.vs : c.ks)[p.vec] = s;
     } else {
         if (!on) return;
-        uint4 o;
-        o.x = pack_bf16(f[0], f[1]);
-        o.y = pack_bf16(f[2], f[3]);
-        o.z = pack_bf16(f[4], f[5]);
-        o.w = pack_bf16(f[6], f[7]);
-        *reinterpret_cast<uint4 *>(pool + (p.vec * c.D + d) * 2) = o;
+        const u32x4 o = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                         pack_bf16(f[6], f[7])};
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(pool + (p.vec * c.D + d) * 2));
     }
 }
 
@@ -209,23 +210,39 @@ hipError_t launch_kv_gather(const KvView &c, bool int8, const KvRows &r, void *k
 // and their scales), i below n or, on the device, below *count.  A workgroup
 // copies up to kCopyChunk bytes of one plane's page per step of a grid-stride
 // loop; bound by memory (each byte read once and written once).
+#ifndef KV_COPY_BLOCKS
+#define KV_COPY_BLOCKS 8192
+#endif
 constexpr int64_t kCopyChunk = 32768;
 
-__device__ __forceinline__ void copy_bytes(uint8_t *d, const uint8_t *s, int64_t bytes) {
-    const uint4 *from = reinterpret_cast<const uint4 *>(s);
-    uint4 *to = reinterpret_cast<uint4 *>(d);
-    const int n = (int)(bytes / 16);
-    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = from[i];
+__device__ __forceinline__ void copy_bytes(uint8_t *d, const uint8_t *s, int bytes) {
+    // 4 loads in flight a thread; each byte is used once
+    constexpr int kStep = 256 * 16;
+    const int at = threadIdx.x * 16;
+    int i = at;
+    for (; i + 3 * kStep < bytes; i += 4 * kStep) {
+        u32x4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s + i + j * kStep));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            __builtin_nontemporal_store(x[j], reinterpret_cast<u32x4 *>(d + i + j * kStep));
+    }
+    for (; i < bytes; i += kStep)
+        __builtin_nontemporal_store(
+            __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s + i)),
+            reinterpret_cast<u32x4 *>(d + i));
 }
 
-__global__ __launch_bounds__(256) void k_kv_copy_pages(KvPlanes D, const int32_t *dst, KvPlanes S,
-                                                       const int32_t *src, int64_t n,
-                                                       const int32_t *count) {
-    const int64_t pairs = count ? min((int64_t)*count, n) : n;
+// Units u0, u0 + step, ... of the copies of `pairs` pages.
+__device__ __forceinline__ void copy_units(const KvPlanes &D, const int32_t *dst,
+                                           const KvPlanes &S, const int32_t *src, int64_t pairs,
+                                           int64_t u0, int64_t step) {
     const int64_t chunks = (S.page_bytes + kCopyChunk - 1) / kCopyChunk;
     const int64_t per_layer = 2 * chunks + (S.scale_bytes ? 2 : 0);
     const int64_t per_pair = per_layer * S.layers;
-    for (int64_t u = blockIdx.x; u < pairs * per_pair; u += gridDim.x) {
+    for (int64_t u = u0; u < pairs * per_pair; u += step) {
         const int64_t i = u / per_pair;
         int64_t x = u - i * per_pair;
         const int from = src[i], to = dst[i];
@@ -240,27 +257,33 @@ __global__ __launch_bounds__(256) void k_kv_copy_pages(KvPlanes D, const int32_t
             const int64_t at = (isv ? x - chunks : x) * kCopyChunk;
             copy_bytes((isv ? D.v : D.k) + tp * S.page_bytes + at,
                        (isv ? S.v : S.k) + fp * S.page_bytes + at,
-                       min(kCopyChunk, S.page_bytes - at));
+                       (int)min(kCopyChunk, S.page_bytes - at));
         } else {
             const bool isv = x > 2 * chunks;
-            copy_bytes(reinterpret_cast<uint8_t *>(isv ? D.vs : D.ks) + tp * S.scale_bytes,
-                       reinterpret_cast<const uint8_t *>(isv ? S.vs : S.ks) + fp * S.scale_bytes,
-                       S.scale_bytes);
+            for (int64_t at = 0; at < S.scale_bytes; at += kCopyChunk)
+                copy_bytes(reinterpret_cast<uint8_t *>(isv ? D.vs : D.ks) + tp * S.scale_bytes + at,
+                           reinterpret_cast<const uint8_t *>(isv ? S.vs : S.ks) +
+                               fp * S.scale_bytes + at,
+                           (int)min(kCopyChunk, S.scale_bytes - at));
         }
     }
 }
 
-static void copy_pages(const KvPlanes &dst, const int32_t *dst_ids, const KvPlanes &src,
-                       const int32_t *src_ids, int64_t n, const int32_t *count, hipStream_t st) {
+__global__ __launch_bounds__(256) void k_kv_copy_pages(KvPlanes D, const int32_t *dst, KvPlanes S,
+                                                       const int32_t *src, int64_t n) {
+    copy_units(D, dst, S, src, n, blockIdx.x, gridDim.x);
+}
+
+// Workgroups for the copies of n pages.
+static int64_t copy_blocks(const KvPlanes &src, int64_t n) {
     const int64_t chunks = (src.page_bytes + kCopyChunk - 1) / kCopyChunk;
-    const int64_t units = n * src.layers * (2 * chunks + (src.scale_bytes ? 2 : 0));
-    hipLaunchKernelGGL(k_kv_copy_pages, dim3((unsigned)std::min<int64_t>(units, 8192)), dim3(256), 0,
-                       st, dst, dst_ids, src, src_ids, n, count);
+    return std::min<int64_t>(n * src.layers * (2 * chunks + (src.scale_bytes ? 2 : 0)), KV_COPY_BLOCKS);
 }
 
 hipError_t launch_kv_copy_pages(const KvPlanes &dst, const int32_t *dst_ids, const KvPlanes &src,
                                 const int32_t *src_ids, int64_t n, hipStream_t st) {
-    copy_pages(dst, dst_ids, src, src_ids, n, nullptr, st);
+    hipLaunchKernelGGL(k_kv_copy_pages, dim3((unsigned)copy_blocks(src, n)), dim3(256), 0, st, dst,
+                       dst_ids, src, src_ids, n);
     return hipGetLastError();
 }
 
@@ -478,13 +501,19 @@ __global__ __launch_bounds__(kPlan) void k_kv_fork_plan(int32_t *table, int64_t 
     }
 }
 
-// Fork, second step: the children's rows and the counts of shared pages.
-__global__ __launch_bounds__(256) void k_kv_fork_rows(int32_t *table, int64_t W, int32_t *refs,
-                                                      int64_t pages, int shift,
-                                                      const int32_t *parents,
-                                                      const int32_t *children, int64_t n,
-                                                      const int32_t *dst, const int32_t *len) {
+// Fork, second step: workgroups 0 .. n - 1 write the children's rows and count the
+// shared pages, the others copy the partial pages.
+__global__ __launch_bounds__(256) void k_kv_fork_apply(KvPlanes c, int32_t *table, int64_t W,
+                                                       int32_t *refs, int shift,
+                                                       const int32_t *parents,
+                                                       const int32_t *children, int64_t n,
+                                                       const int32_t *src, const int32_t *dst,
+                                                       const int32_t *len) {
     const int64_t i = blockIdx.x;
+    if (i >= n) {
+        copy_units(c, dst, c, src, n, i - n, gridDim.x - n);
+        return;
+    }
     const int l = len[i];
     if (l < 0) return;
     const int64_t full = l >> shift;
@@ -494,7 +523,7 @@ __global__ __launch_bounds__(256) void k_kv_fork_rows(int32_t *table, int64_t W,
         int p = -1;
         if (j < full) {
             p = from[j];
-            if (p >= 0 && p < pages) atomicAdd(&refs[p], 1);
+            if (p >= 0 && p < c.pages) atomicAdd(&refs[p], 1);
         } else if (j == full) {
             p = dst[i];
         }
@@ -509,9 +538,8 @@ hipError_t launch_kv_fork(const KvPlanes &c, int shift, int32_t *table, int64_t 
     int32_t *src = ws, *dst = ws + n, *len = ws + 2 * n, *upto = ws + 3 * n;
     hipLaunchKernelGGL(k_kv_fork_plan, dim3(1), dim3(kPlan), 0, st, table, S, W, lens, refs,
                        c.pages, shift, parents, children, n, ok, src, dst, len, upto);
-    hipLaunchKernelGGL(k_kv_fork_rows, dim3((unsigned)n), dim3(256), 0, st, table, W, refs,
-                       c.pages, shift, parents, children, n, dst, len);
-    copy_pages(c, dst, c, src, n, nullptr, st);
+    hipLaunchKernelGGL(k_kv_fork_apply, dim3((unsigned)(n + copy_blocks(c, n))), dim3(256), 0, st,
+                       c, table, W, refs, shift, parents, children, n, src, dst, len);
     return hipGetLastError();
 }
 
@@ -577,21 +605,27 @@ __global__ __launch_bounds__(kPlan) void k_kv_compact_plan(const int32_t *refs, 
     }
 }
 
-// Compaction, second step: the tables' entries; a moved page's new place is
-// found in the sorted list of moves.
-__global__ __launch_bounds__(256) void k_kv_compact_table(const int32_t *table,
+// Compaction, second step: the first `tables` workgroups rename the table's
+// entries (a moved page's new place is found in the sorted list of moves), the
+// others copy the pages.
+__global__ __launch_bounds__(256) void k_kv_compact_apply(KvPlanes c, const int32_t *table,
                                                           int32_t *table_out, int64_t entries,
-                                                          int64_t pages, const int32_t *live,
+                                                          int64_t tables, const int32_t *live,
                                                           const int32_t *moves,
                                                           const int32_t *src,
                                                           const int32_t *dst) {
+    const int n = moves[0];
+    if (blockIdx.x >= tables) {
+        copy_units(c, dst, c, src, n, blockIdx.x - tables, gridDim.x - tables);
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= entries) return;
     int p = table[i];
-    if (p < 0 || p >= pages) {
+    if (p < 0 || p >= c.pages) {
         p = -1;
     } else if (p >= live[0]) {
-        int lo = 0, hi = moves[0];
+        int lo = 0, hi = n;
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
             if (src[mid] < p)
@@ -599,7 +633,7 @@ __global__ __launch_bounds__(256) void k_kv_compact_table(const int32_t *table,
             else
                 hi = mid;
         }
-        if (lo < moves[0] && src[lo] == p) p = dst[lo];
+        if (lo < n && src[lo] == p) p = dst[lo];
     }
     table_out[i] = p;
 }
@@ -610,10 +644,11 @@ hipError_t launch_kv_compact(const KvPlanes &c, const int32_t *table, int64_t S,
     int32_t *moves = ws, *src = ws + 4, *dst = src + c.pages;
     hipLaunchKernelGGL(k_kv_compact_plan, dim3(1), dim3(kPlan), 0, st, refs, refs_out, c.pages,
                        live, moves, src, dst);
-    hipLaunchKernelGGL(k_kv_compact_table, dim3((unsigned)((S * W + 255) / 256)), dim3(256), 0,
-                       st, table, table_out, S * W, c.pages, live, moves, src, dst);
     // at most half of the pages move (a move needs a live page and a hole)
-    copy_pages(c, dst, c, src, c.pages / 2 > 0 ? c.pages / 2 : 1, moves, st);
+    const int64_t tables = (S * W + 255) / 256;
+    const int64_t blocks = tables + copy_blocks(c, std::max<int64_t>(c.pages / 2, 1));
+    hipLaunchKernelGGL(k_kv_compact_apply, dim3((unsigned)blocks), dim3(256), 0, st, c, table,
+                       table_out, S * W, tables, live, moves, src, dst);
     return hipGetLastError();
 }
 

@@ -555,9 +555,18 @@ __global__ __launch_bounds__(256) void k_kv_prefill_join(KvAttnArgs a, int parts
     const int d = threadIdx.x % lanes * 4;
     float m = -INFINITY, l = 0.0f;
     float4 y = {};
-    for (int i = 0; i < parts; ++i) {
-        const float *p = RowOut{row, i, parts}.sums(a);
-        add_part(m, l, y, p[D], p[D + 1], *reinterpret_cast<const float4 *>(p + d));
+    for (int i = 0; i < parts; i += 4) {  // (four parts' loads at a time)
+        float mk[4], lk[4];
+        float4 z[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float *p = RowOut{row, min(i + x, parts - 1), parts}.sums(a);
+            mk[x] = i + x < parts ? p[D] : -INFINITY;
+            lk[x] = p[D + 1];
+            z[x] = *reinterpret_cast<const float4 *>(p + d);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) add_part(m, l, y, mk[x], lk[x], z[x]);
     }
     store_out<FP32>(a.out, row * D + d, y, l);
 }

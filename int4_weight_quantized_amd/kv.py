@@ -139,14 +139,16 @@ def _rows(x: torch.Tensor, name: str, heads, head_dim: int, dev, dtype=None):
         raise ValueError(f"{name} is on {x.device}, the cache on {dev}")
     if x.dtype not in _XTYPES or (dtype is not None and x.dtype != dtype):
         raise TypeError(f"{name} must be {dtype or 'bfloat16 or float32'}, got {x.dtype}")
-    if x.shape[2] != head_dim or (heads is not None and x.shape[1] != heads):
+    n, h, d = x.shape
+    if d != head_dim or (heads is not None and h != heads):
         raise ValueError(f"{name} must have shape (tokens, {heads or 'heads'}, {head_dim}), got "
                          f"{tuple(x.shape)}")
+    if x.is_contiguous():
+        return x.data_ptr(), h * d
     s = x.stride()
-    if s[2] != 1 or (s[1] != head_dim and x.shape[1] > 1):
+    if s[2] != 1 or (s[1] != d and h > 1):
         raise ValueError(f"{name}'s heads and values must be contiguous")
-    row = x.shape[1] * head_dim
-    return x.data_ptr(), s[0] if x.shape[0] > 1 else row
+    return x.data_ptr(), s[0] if n > 1 else h * d
 
 
 def _empty(shape, dtype, dev, stream):
@@ -192,6 +194,8 @@ def kv_gather(cache: KVCache, layer: int, table: torch.Tensor, start: torch.Tens
     shape = (tokens, c.heads, c.head_dim)
     if dtype not in _XTYPES:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    if k is None and v is None:
+        k, v = _empty((2,) + shape, dtype, dev, stream).unbind(0)
     k = _empty(shape, dtype, dev, stream) if k is None else k
     v = _empty(shape, dtype, dev, stream) if v is None else v
     pt, B, W = _table(table, None, dev)
