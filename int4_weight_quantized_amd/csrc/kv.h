@@ -7,11 +7,20 @@
 #include <stdint.h>
 
 #include "../../include/w4.h"
+#include "kernels.h"
 
 namespace w4 {
 
 // Record the outcome of a launch as the C ABI's status (api.cpp).
 int finish_call(const char *path, hipError_t e);
+
+// Launch a call's main kernel, and remember it as the one that the call ran.
+template <typename... KArgs, typename... Args>
+inline void launch_kv(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t lds, hipStream_t st,
+                      Args... args) {
+    note_kernel(reinterpret_cast<const void *>(kernel), st);
+    hipLaunchKernelGGL(kernel, grid, block, lds, st, KArgs(args)...);
+}
 
 // One layer of a cache and the page table of a call, as the kernels take them.
 struct KvView {
@@ -50,7 +59,8 @@ struct KvAttnArgs {
 };
 
 size_t kv_attn_ws_bytes(int64_t rows, int64_t B, int64_t hq, int64_t heads, int64_t D);
-hipError_t launch_kv_attention(const KvAttnArgs &a, hipStream_t st);
+// `path`: the kernel variant taken.
+hipError_t launch_kv_attention(const KvAttnArgs &a, const char **path, hipStream_t st);
 
 // Page moves: the cache's arrays as planes of whole pages.
 struct KvPlanes {

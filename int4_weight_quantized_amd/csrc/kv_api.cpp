@@ -115,7 +115,7 @@ int check_rows(const kv_cache *c, int64_t layer, const void *k, const void *v, i
     return W4_OK;
 }
 
-int attention(const char *path, const kv_cache *c, int64_t layer, const void *q, int x_dtype,
+int attention(const kv_cache *c, int64_t layer, const void *q, int x_dtype,
               int64_t ldq, int64_t T, int64_t B, int64_t hq, const int32_t *table, int64_t W,
               const int32_t *lens, const int32_t *cu, float scale, int64_t window, int64_t sinks,
               void *out, void *workspace, size_t workspace_bytes, void *stream) {
@@ -153,7 +153,9 @@ int attention(const char *path, const kv_cache *c, int64_t layer, const void *q,
     a.window = (int)std::min(window, kMaxTokens);
     a.sinks = (int)std::min(sinks, kMaxTokens);
     a.ws = workspace;
-    return w4::finish_call(path, w4::launch_kv_attention(a, hip_stream(stream)));
+    const char *path = "none";
+    const hipError_t e = w4::launch_kv_attention(a, &path, hip_stream(stream));
+    return w4::finish_call(path, e);
 }
 
 }  // namespace
@@ -202,7 +204,7 @@ int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int
                         int64_t W, const int32_t *lens, float scale, int64_t window,
                         int64_t sinks, void *out, void *workspace, size_t workspace_bytes,
                         void *stream) {
-    return attention("kv_decode", cache, layer, q, x_dtype, q_stride, B, B, q_heads, table, W,
+    return attention(cache, layer, q, x_dtype, q_stride, B, B, q_heads, table, W,
                      lens, nullptr, scale, window, sinks, out, workspace, workspace_bytes,
                      stream);
 }
@@ -213,7 +215,7 @@ int kv_prefill_attention(const kv_cache *cache, int64_t layer, const void *q, in
                          const int32_t *cu, float scale, int64_t window, int64_t sinks,
                          void *out, void *workspace, size_t workspace_bytes, void *stream) {
     if (!cu) return W4_ERR_NULL;
-    return attention("kv_prefill", cache, layer, q, x_dtype, q_stride, T, B, q_heads, table, W,
+    return attention(cache, layer, q, x_dtype, q_stride, T, B, q_heads, table, W,
                      lens, cu, scale, window, sinks, out, workspace, workspace_bytes, stream);
 }
 

@@ -7,8 +7,8 @@ size_t kv_attn_ws_bytes(int64_t rows, int64_t B, int64_t hq, int64_t heads, int6
     return std::max(kv_decode_ws_bytes(hq, heads, D), kv_prefill_ws_bytes(rows, B, hq, heads, D));
 }
 
-hipError_t launch_kv_attention(const KvAttnArgs &a, hipStream_t st) {
-    return a.cu ? launch_kv_prefill(a, st) : launch_kv_decode(a, st);
+hipError_t launch_kv_attention(const KvAttnArgs &a, const char **path, hipStream_t st) {
+    return a.cu ? launch_kv_prefill(a, path, st) : launch_kv_decode(a, path, st);
 }
 
 }  // namespace w4

@@ -182,8 +182,8 @@ hipError_t launch_kv_append(const KvView &c, bool int8, const KvRows &r, const v
             with_bool(fp32, [&](auto f32) {
                 constexpr int L = decltype(lanes)::value;
                 const dim3 g((unsigned)((r.T * c.heads + 256 / L - 1) / (256 / L)), 2);
-                hipLaunchKernelGGL((k_kv_append<decltype(i8)::value, decltype(f32)::value, L>), g,
-                                   dim3(256), 0, st, c, r, k, v, ldk, ldv, vec);
+                launch_kv(k_kv_append<decltype(i8)::value, decltype(f32)::value, L>, g, dim3(256),
+                          0, st, c, r, k, v, ldk, ldv, vec);
             });
         });
     });
@@ -197,8 +197,8 @@ hipError_t launch_kv_gather(const KvView &c, bool int8, const KvRows &r, void *k
             with_bool(fp32, [&](auto f32) {
                 constexpr int L = decltype(lanes)::value;
                 const dim3 g((unsigned)((r.T * c.heads + 256 / L - 1) / (256 / L)), 2);
-                hipLaunchKernelGGL((k_kv_gather<decltype(i8)::value, decltype(f32)::value, L>), g,
-                                   dim3(256), 0, st, c, r, k, v);
+                launch_kv(k_kv_gather<decltype(i8)::value, decltype(f32)::value, L>, g, dim3(256),
+                          0, st, c, r, k, v);
             });
         });
     });
@@ -282,7 +282,7 @@ static int64_t copy_blocks(const KvPlanes &src, int64_t n) {
 
 hipError_t launch_kv_copy_pages(const KvPlanes &dst, const int32_t *dst_ids, const KvPlanes &src,
                                 const int32_t *src_ids, int64_t n, hipStream_t st) {
-    hipLaunchKernelGGL(k_kv_copy_pages, dim3((unsigned)copy_blocks(src, n)), dim3(256), 0, st, dst,
+    launch_kv(k_kv_copy_pages, dim3((unsigned)copy_blocks(src, n)), dim3(256), 0, st, dst,
                        dst_ids, src, src_ids, n);
     return hipGetLastError();
 }
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(int32_t *table, int64_t S,
 hipError_t launch_kv_reserve(int32_t *table, int64_t S, int64_t W, const int32_t *lens,
                              int32_t *refs, int64_t pages, int shift, const int32_t *add,
                              int32_t *ok, int32_t *ws, hipStream_t st) {
-    hipLaunchKernelGGL(k_kv_reserve, dim3(1), dim3(kPlan), 0, st, table, S, W, lens, refs, pages,
+    launch_kv(k_kv_reserve, dim3(1), dim3(kPlan), 0, st, table, S, W, lens, refs, pages,
                        shift, add, ok, ws, ws + S);
     return hipGetLastError();
 }
@@ -536,7 +536,7 @@ hipError_t launch_kv_fork(const KvPlanes &c, int shift, int32_t *table, int64_t 
                           const int32_t *children, int64_t n, int32_t *ok, int32_t *ws,
                           hipStream_t st) {
     int32_t *src = ws, *dst = ws + n, *len = ws + 2 * n, *upto = ws + 3 * n;
-    hipLaunchKernelGGL(k_kv_fork_plan, dim3(1), dim3(kPlan), 0, st, table, S, W, lens, refs,
+    launch_kv(k_kv_fork_plan, dim3(1), dim3(kPlan), 0, st, table, S, W, lens, refs,
                        c.pages, shift, parents, children, n, ok, src, dst, len, upto);
     hipLaunchKernelGGL(k_kv_fork_apply, dim3((unsigned)(n + copy_blocks(c, n))), dim3(256), 0, st,
                        c, table, W, refs, shift, parents, children, n, src, dst, len);
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(256) void k_kv_free(int32_t *table, int64_t S, int6
 
 hipError_t launch_kv_free(int32_t *table, int64_t S, int64_t W, int32_t *lens, int32_t *refs,
                           int64_t pages, const int32_t *slots, int64_t n, hipStream_t st) {
-    hipLaunchKernelGGL(k_kv_free, dim3((unsigned)n), dim3(256), 0, st, table, S, W, lens, refs,
+    launch_kv(k_kv_free, dim3((unsigned)n), dim3(256), 0, st, table, S, W, lens, refs,
                        pages, slots, n);
     return hipGetLastError();
 }
@@ -642,7 +642,7 @@ hipError_t launch_kv_compact(const KvPlanes &c, const int32_t *table, int64_t S,
                              const int32_t *refs, int32_t *table_out, int32_t *refs_out,
                              int32_t *live, int32_t *ws, hipStream_t st) {
     int32_t *moves = ws, *src = ws + 4, *dst = src + c.pages;
-    hipLaunchKernelGGL(k_kv_compact_plan, dim3(1), dim3(kPlan), 0, st, refs, refs_out, c.pages,
+    launch_kv(k_kv_compact_plan, dim3(1), dim3(kPlan), 0, st, refs, refs_out, c.pages,
                        live, moves, src, dst);
     // at most half of the pages move (a move needs a live page and a hole)
     const int64_t tables = (S * W + 255) / 256;

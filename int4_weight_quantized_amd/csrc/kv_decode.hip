@@ -604,7 +604,7 @@ size_t lds_bytes(int waves, int rows) {
 }
 
 template <int DP, bool INT8, bool FP32, bool PACK>
-hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
+hipError_t launch_dp(const KvAttnArgs &a, const char **path, hipStream_t st) {
     const KvHeads hd(a);
     const int64_t pairs = a.B * hd.count;
     // Tokens of the longest sequence that the table can hold and the window shows
@@ -614,11 +614,13 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
         constexpr int kWholeWaves = DP == 256 && FP32 && !PACK ? 4 : 8;  // (registers)
         const size_t lds = lds_bytes<DP, INT8>(kWholeWaves, hd.rows);
         auto *k = k_kv_decode<DP, INT8, FP32, PACK, kWholeWaves, false>;
-        hipLaunchKernelGGL(k, dim3((unsigned)pairs), dim3(kWholeWaves * 64), lds, st, a);
+        *path = "kv_decode";
+        launch_kv(k, dim3((unsigned)pairs), dim3(kWholeWaves * 64), lds, st, a);
     } else {
         const size_t lds = lds_bytes<DP, INT8>(kSplitWaves, hd.rows);
         auto *k = k_kv_decode<DP, INT8, FP32, PACK, kSplitWaves, true>;
-        hipLaunchKernelGGL(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
+        *path = "kv_decode_split";
+        launch_kv(k, dim3(kSplitBlocks), dim3(kSplitWaves * 64), lds, st, a);
         hipLaunchKernelGGL((k_kv_decode_join<DP, FP32>), dim3(kSplitBlocks, hd.rows), dim3(256), 0,
                            st, a);
     }
@@ -626,16 +628,16 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
 }
 
 template <int DP, bool INT8, bool FP32>
-hipError_t launch_group(const KvAttnArgs &a, hipStream_t st) {
-    return a.hq / a.c.heads <= (FP32 ? 4 : 8) ? launch_dp<DP, INT8, FP32, true>(a, st)
-                                              : launch_dp<DP, INT8, FP32, false>(a, st);
+hipError_t launch_group(const KvAttnArgs &a, const char **path, hipStream_t st) {
+    return a.hq / a.c.heads <= (FP32 ? 4 : 8) ? launch_dp<DP, INT8, FP32, true>(a, path, st)
+                                              : launch_dp<DP, INT8, FP32, false>(a, path, st);
 }
 
 template <int DP>
-hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
+hipError_t launch_types(const KvAttnArgs &a, const char **path, hipStream_t st) {
     if (a.int8)
-        return a.fp32 ? launch_group<DP, true, true>(a, st) : launch_group<DP, true, false>(a, st);
-    return a.fp32 ? launch_group<DP, false, true>(a, st) : launch_group<DP, false, false>(a, st);
+        return a.fp32 ? launch_group<DP, true, true>(a, path, st) : launch_group<DP, true, false>(a, path, st);
+    return a.fp32 ? launch_group<DP, false, true>(a, path, st) : launch_group<DP, false, false>(a, path, st);
 }
 
 }  // namespace
@@ -646,10 +648,10 @@ size_t kv_decode_ws_bytes(int64_t hq, int64_t heads, int64_t D) {
     return (size_t)(kSplitBlocks * (16 + 2 * rows * (DP + 4) * 4));
 }
 
-hipError_t launch_kv_decode(const KvAttnArgs &a, hipStream_t st) {
-    return a.c.D <= 64 ? launch_types<64>(a, st)
-           : a.c.D <= 128 ? launch_types<128>(a, st)
-                          : launch_types<256>(a, st);
+hipError_t launch_kv_decode(const KvAttnArgs &a, const char **path, hipStream_t st) {
+    return a.c.D <= 64 ? launch_types<64>(a, path, st)
+           : a.c.D <= 128 ? launch_types<128>(a, path, st)
+                          : launch_types<256>(a, path, st);
 }
 
 }  // namespace w4

@@ -586,7 +586,7 @@ int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
 }
 
 template <int DP, bool INT8, bool FP32>
-hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
+hipError_t launch_dp(const KvAttnArgs &a, const char **path, hipStream_t st) {
     const int64_t groups = row_tiles(a.T, a.B, a.hq / a.c.heads) * a.c.heads;
     // tiles of the longest sequence that the table can hold and the window shows
     int64_t most = a.c.W << a.c.shift;
@@ -594,8 +594,9 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
     const int parts = (int)std::min(most_parts(a.T, a.B, a.hq, a.c.heads), (most + kTile - 1) / kTile);
     const size_t tile_bytes = 2 * 2 * kTile * DP * 2;
     const size_t out_bytes = kRows * (DP * (FP32 ? 4 : 2) + 16);
-    hipLaunchKernelGGL((k_kv_prefill<DP, INT8, FP32>), dim3((unsigned)groups, parts),
-                       dim3(kThreads), std::max(tile_bytes, out_bytes), st, a, parts);
+    *path = parts > 1 ? "kv_prefill_split" : "kv_prefill";
+    launch_kv(k_kv_prefill<DP, INT8, FP32>, dim3((unsigned)groups, parts), dim3(kThreads),
+              std::max(tile_bytes, out_bytes), st, a, parts);
     if (parts > 1) {
         const int rows = 256 / (a.c.D / 4);
         hipLaunchKernelGGL(k_kv_prefill_join<FP32>,
@@ -606,9 +607,9 @@ hipError_t launch_dp(const KvAttnArgs &a, hipStream_t st) {
 }
 
 template <int DP>
-hipError_t launch_types(const KvAttnArgs &a, hipStream_t st) {
-    if (a.int8) return a.fp32 ? launch_dp<DP, true, true>(a, st) : launch_dp<DP, true, false>(a, st);
-    return a.fp32 ? launch_dp<DP, false, true>(a, st) : launch_dp<DP, false, false>(a, st);
+hipError_t launch_types(const KvAttnArgs &a, const char **path, hipStream_t st) {
+    if (a.int8) return a.fp32 ? launch_dp<DP, true, true>(a, path, st) : launch_dp<DP, true, false>(a, path, st);
+    return a.fp32 ? launch_dp<DP, false, true>(a, path, st) : launch_dp<DP, false, false>(a, path, st);
 }
 
 }  // namespace
@@ -618,10 +619,10 @@ size_t kv_prefill_ws_bytes(int64_t T, int64_t B, int64_t hq, int64_t heads, int6
     return parts > 1 ? (size_t)(T * hq * parts * (D + 4) * 4) : 0;
 }
 
-hipError_t launch_kv_prefill(const KvAttnArgs &a, hipStream_t st) {
-    return a.c.D <= 64 ? launch_types<64>(a, st)
-           : a.c.D <= 128 ? launch_types<128>(a, st)
-                          : launch_types<256>(a, st);
+hipError_t launch_kv_prefill(const KvAttnArgs &a, const char **path, hipStream_t st) {
+    return a.c.D <= 64 ? launch_types<64>(a, path, st)
+           : a.c.D <= 128 ? launch_types<128>(a, path, st)
+                          : launch_types<256>(a, path, st);
 }
 
 }  // namespace w4

@@ -291,3 +291,84 @@ def test_attention_in_a_graph_and_on_another_stream(w4):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager) and torch.equal(outp, wantp)
+
+
+def test_paths(w4):
+    """The variants that the sizes select."""
+    def decode(lens, W):
+        cache, table, tl, K, V = make_cache(w4, lens, 2, 16, 64, "bf16", 40, W=W)
+        w4.kv_decode_attention(make_q((len(lens), 4, 64), "fp32", 40), cache, 0, table, tl)
+        return w4.w4_last_path(), w4.w4_last_kernel()
+
+    def prefill(B, new):
+        cache, table, tl, K, V = make_cache(w4, [new] * B, 2, 16, 64, "bf16", 41)
+        cu = torch.arange(0, B * new + 1, new, dtype=torch.int32).cuda()
+        w4.kv_prefill_attention(make_q((B * new, 4, 64), "bf16", 41), cache, 0, table, tl, cu)
+        return w4.w4_last_path(), w4.w4_last_kernel()
+
+    for (path, kernel), want in ((decode([5, 9], 8), "kv_decode"),
+                                 (decode([5, 9], 200), "kv_decode_split"),
+                                 (prefill(2, 200), "kv_prefill_split"),
+                                 (prefill(300, 3), "kv_prefill")):
+        assert path == want and "k_" + want.replace("_split", "") in kernel
+
+
+def test_many_sequences(w4):
+    """More sequences than a wave has lanes, at every place that searches them."""
+    lens = [(i * 37) % 90 for i in range(200)]
+    lens[150] = 4000
+    check_decode(w4, lens, 4, 2, 64, 16, "bf16", "fp32", seed=42)
+    pairs = [(n, min(n, i % 4)) for i, n in enumerate(lens)]
+    check_prefill(w4, pairs, 4, 2, 64, 16, "int8", "fp32", seed=43)
+
+
+@pytest.mark.parametrize("q", ["bf16", "fp32"])
+@pytest.mark.parametrize("pairs", [[(400, 6)], [(90, 90)] * 12])
+def test_prefill_hidden_infinities_split(w4, q, pairs):
+    """The same as test_prefill_future_infinities for more layouts of the work,
+    infinities in several tiles, a missing page among them."""
+    hq, heads, D, ps = 4, 1, 128, 16
+    lens = [n for n, _ in pairs]
+    cache, table, tl, K, V = make_cache(w4, lens, heads, ps, D, "bf16", 44)
+    cu = [0]
+    for _, m in pairs:
+        cu.append(cu[-1] + m)
+    x = make_q((cu[-1], hq, D), q, 44)
+    n, m = pairs[-1]
+    bad = [n - 1, n - 3]
+    for t in bad:
+        page, slot = int(table[-1, t // ps]), t % ps
+        cache.k[0, page, :, slot] = math.nan
+        cache.v[0, page, :, slot, ::3] = -math.inf
+    t = table.clone()
+    t[-1, 1] = -1
+    y = w4.kv_prefill_attention(x, cache, 0, t, tl, torch.tensor(cu, dtype=torch.int32).cuda())
+    hole = torch.zeros(n, dtype=torch.bool)
+    hole[ps:2 * ps] = True
+    for i in bad:
+        K[-1][i] = 0
+        V[-1][i] = 0
+    out, rel, mean = attend(x[cu[-2]:], K[-1], V[-1], range(n - m, n), 0, 0, D ** -0.5, hole)
+    rows = m - 3
+    ok, worst = close(y[cu[-2]:][:rows], out[:rows], rel[:rows], mean[:rows], p_rounded=q == "bf16")
+    assert ok, worst
+    assert not torch.isfinite(y[-1]).all()
+
+
+def test_prefill_unequal_scales(w4):
+    """int8: scales of hidden tokens that are infinite or NaN reach nothing."""
+    n = 150
+    cache, table, tl, K, V = make_cache(w4, [n], 2, 16, 64, "int8", 45)
+    x = make_q((n, 4, 64), "bf16", 45)
+    for t, val in ((100, math.inf), (30, math.nan)):
+        page, slot = int(table[0, t // 16]), t % 16
+        cache.k_scale[0, page, :, slot] = val
+        cache.v_scale[0, page, :, slot] = val
+        K[0][t] = 0
+        V[0][t] = 0
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    y = w4.kv_prefill_attention(x, cache, 0, table, tl, cu, window=40, sinks=2)
+    clean = [p for p in range(n) if not any(t <= p < t + 40 for t in (100, 30))]
+    out, rel, mean = attend(x, K[0], V[0], range(n), 40, 2, 0.125)
+    ok, worst = close(y[clean], out[clean], rel[clean], mean[clean], p_rounded=True)
+    assert ok, worst
