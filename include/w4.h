@@ -370,8 +370,9 @@ int w4a8_linear_prepacked(const float *X, int64_t M, int64_t K, int64_t N,
  *            (KV_BF16) or int8 codes (KV_INT8);
  *   k_scale, v_scale  [layers][pages][heads][page_size] fp32, one scale for
  *            each token and head (KV_INT8; NULL for KV_BF16): the value is
- *            code * scale, quantized by the rule of a8_quantize_act with a
- *            head's vector as the row;
+ *            code * scale, scale = fl(max_d |x[d]| * fl(1 / 127)) of the head's
+ *            vector, code = clamp(rne(fl(x / scale)), -128, 127) (0 where the
+ *            scale is 0): a8_quantize_act's rule but for the scale's last bit;
  *   table    [S][W] int32: entry j of a row is the page of tokens
  *            j * page_size ... (j + 1) * page_size - 1, -1 where there is none;
  *   lens     [S] int32, cached tokens; refs [pages] int32, how many rows hold

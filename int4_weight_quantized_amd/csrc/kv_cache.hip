@@ -75,8 +75,9 @@ __device__ __forceinline__ void load8(const void *x, int64_t at, bool vec, float
     }
 }
 
-// Rounding to the cache's type happens once, here: bf16 half to even, or the
-// int8 rule of the activation quantizer (absmax / 127 of the head's vector).
+// Rounding to the cache's type happens once, here: bf16 half to even, or int8 with
+// the scale absmax * fl(1 / 127) of the head's vector (one multiplication, within
+// one unit in the last place of the quotient) and codes rne(fl(x / scale)).
 template <bool INT8, bool FP32, int LPV>
 __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const void *k,
                                                    const void *v, int64_t ldk, int64_t ldv,
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
 #pragma unroll
         for (int o = LPV / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
         if (!on) return;
-        const float s = div127(m);
+        const float s = m * (1.0f / 127.0f);
         uint32_t w[2] = {};
 #pragma unroll
         for (int j = 0; j < 8; ++j)

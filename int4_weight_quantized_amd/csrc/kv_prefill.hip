@@ -77,10 +77,11 @@ __device__ __forceinline__ int64_t find_tile(const KvAttnArgs &a, int G, int64_t
     return lo;
 }
 
-// Sum of a packed bf16 pair and c.
-__device__ __forceinline__ float add_pair(uint32_t w, float c) {
-    const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), one, c, false);
+// c + the products of two packed bf16 pairs (`one`: both 1).
+constexpr uint32_t one = 0x3F803F80u;
+__device__ __forceinline__ float dot_pair(uint32_t w, uint32_t x, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w),
+                                           __builtin_bit_cast(bf16x2, x), c, false);
 }
 
 // Where a row's result goes: to its place in the output, or, where the tiles of a
@@ -171,6 +172,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     constexpr int kLoads = INT8 ? DP / 64 : DP / 32;  // loads of 16 rows by a wave
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ float sks[2][kTile], svs[2][kTile];
+    __shared__ __align__(8) uint16_t inv_hi[2][kTile], inv_lo[2][kTile];  // 1 / svs, two bf16 terms
     __shared__ int odd;  // whether a tile at an edge has values of V that are not finite
 
     const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
@@ -301,9 +303,19 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 }
             }
             if (lane < 16) {
-                sks[buf][wave * 16 + lane] = ks;
-                // (finite, so that an unseen token's weight of zero stays zero)
-                svs[buf][wave * 16 + lane] = fminf(vs, 3.0e38f);
+                const int at = wave * 16 + lane;
+                sks[buf][at] = ks;
+                // (finite, so that an unseen token's weight of zero stays zero, and not
+                // zero, so that it can be divided by: codes times 2^-100 count nothing)
+                float v = fminf(vs, 3.0e38f);
+                if (fabsf(v) < 0x1p-100f) v = 0x1p-100f;
+                svs[buf][at] = v;
+                if constexpr (!FP32) {
+                    const float inv = 1.0f / v;
+                    const uint32_t hi = pack_bf16(inv, 0.0f);
+                    inv_hi[buf][at] = (uint16_t)hi;
+                    inv_lo[buf][at] = (uint16_t)pack_bf16(inv - bf16_lo(hi), 0.0f);
+                }
             }
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -449,7 +461,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
             for (int j = 0; j < 8; ++j)
                 f[j] = __builtin_amdgcn_exp2f(
                     __builtin_fmaf(s[i4 / 2][8 * (i4 % 2) + j], sc, mu));
-            if constexpr (INT8 || FP32) {
+            if constexpr (FP32) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) l += f[j];
             }
@@ -464,12 +476,26 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
             }
             uint4 p[kP];
             split_bf16<kP>(f, p);
-            if constexpr (!INT8 && !FP32) {
-                // (the sum of the rounded weights, as the product takes them)
-                l = add_pair(p[0].x, l);
-                l = add_pair(p[0].y, l);
-                l = add_pair(p[0].z, l);
-                l = add_pair(p[0].w, l);
+            // the sum of the weights as the product takes them, rounded (and their
+            // scales divided out): what rounding does to a weight that outweighs the
+            // others cancels in O / l
+            if constexpr (!FP32) {
+                const uint32_t w[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+#pragma unroll
+                for (int j4 = 0; j4 < 2; ++j4) {
+                    if constexpr (INT8) {
+                        const int at = 16 * i4 + 8 * j4 + 4 * half;
+                        const uint2 h = *reinterpret_cast<const uint2 *>(&inv_hi[buf][at]);
+                        const uint2 x = *reinterpret_cast<const uint2 *>(&inv_lo[buf][at]);
+                        l = dot_pair(w[2 * j4], x.x, l);
+                        l = dot_pair(w[2 * j4 + 1], x.y, l);
+                        l = dot_pair(w[2 * j4], h.x, l);
+                        l = dot_pair(w[2 * j4 + 1], h.y, l);
+                    } else {
+                        l = dot_pair(w[2 * j4], one, l);
+                        l = dot_pair(w[2 * j4 + 1], one, l);
+                    }
+                }
             }
 #pragma unroll
             for (int d = 0; d < kDt; ++d) {

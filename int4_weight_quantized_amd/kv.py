@@ -4,8 +4,8 @@ What a decoder layer runs between its quantized projections.  A cache holds K
 and V of every layer in pages; a sequence (slot) owns a row of a page table:
 
 * ``KVCache``              -- the cache's arrays, checked once;
-* ``kv_append``            -- write new tokens (bf16, or int8 by the activation
-  quantizer's rule with one scale per token and head);
+* ``kv_append``            -- write new tokens (bf16, or int8 codes with one
+  absmax / 127 scale per token and head);
 * ``kv_gather``            -- read tokens back as contiguous values;
 * ``kv_decode_attention``  -- attention of one new token per sequence;
 * ``kv_prefill_attention`` -- attention of prompts or chunks of them; both with

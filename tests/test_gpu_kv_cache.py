@@ -15,6 +15,9 @@ def w4():
     return pkg
 
 
+INV127 = torch.tensor(1.0 / 127.0, dtype=torch.float32)
+
+
 def ints(v):
     return torch.tensor(v, dtype=torch.int32).cuda()
 
@@ -40,7 +43,7 @@ def arrays(c):
 
 # ------------------------------------------------------------------- append
 def plain_append(c, layer, k, v, table, start, cu):
-    """The host form, in place on copies of the arrays: exact fp32 divisions."""
+    """The host form, in place on copies of the arrays: fp32 product and division."""
     pools = [t.clone().cpu() for t in arrays(c)]
     table, start = table.tolist(), start.tolist()
     rows = [(b, p, r) for b in range(len(start))
@@ -56,7 +59,7 @@ def plain_append(c, layer, k, v, table, start, cu):
             slot = (start[b] + p) % c.page_size
             if c.int8:
                 f = x[r].float()
-                s = f.abs().amax(-1) / 127
+                s = f.abs().amax(-1) * INV127
                 q = torch.where(s[:, None] > 0, torch.round(f / s[:, None]).clamp(-128, 127), 0.0)
                 pools[which][layer, page, :, slot] = q.to(torch.int8)
                 pools[2 + which][layer, page, :, slot] = s
@@ -154,13 +157,33 @@ def test_append_strides(w4, dt, kv):
 
 
 def test_append_quantizes_like_the_activation_quantizer(w4):
+    """The same codes and scales but for the scale's last bit, which can move a
+    code where the quotient is next to a half."""
     x = (torch.randn((50, 128)) * torch.logspace(-3, 3, 50)[:, None]).cuda()
     c = w4.KVCache.empty(1, 4, 1, 16, 128, torch.int8)
     w4.kv_append(c, 0, x[:, None], x[:, None], ints([[2, 0, 3, 1]]), ints([0]), ints([0, 50]))
     q, s = w4.a8_quantize_act(x)
     pages = torch.tensor([2, 0, 3, 1]).cuda()
-    assert torch.equal(c.k[0, pages, 0].reshape(64, 128)[:50], q)
-    assert torch.equal(c.v_scale[0, pages, 0].reshape(64)[:50], s)
+    codes = c.k[0, pages, 0].reshape(64, 128)[:50]
+    scales = c.v_scale[0, pages, 0].reshape(64)[:50]
+    assert bool(((scales - s).abs() <= s * 2.0 ** -23).all())
+    t = x.double() / s.double()[:, None]
+    near = ((t - t.floor()) - 0.5).abs() < 1e-4
+    assert torch.equal(codes[~near], q[~near])
+    assert bool(((codes.int() - q.int()).abs() <= 1).all())
+
+
+@pytest.mark.parametrize("kv_in", [torch.bfloat16, torch.float32])
+def test_append_ties(w4, kv_in):
+    """Values at half codes: bf16 rows of few distinct values, bit for bit."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randint(-8, 9, (600, 2, 64), generator=g).float().div(16).to(kv_in).cuda()
+    c = random_pool(w4, 1, 40, 2, 16, 64, "int8", 10)
+    table = torch.randperm(40, generator=g)[:38].int().cuda()[None].contiguous()
+    want = plain_append(c, 0, x, x, table, ints([0]), [0, 600])
+    w4.kv_append(c, 0, x, x, table, ints([0]), ints([0, 600]))
+    for a, b in zip(arrays(c), want):
+        assert torch.equal(bits(a.cpu()), bits(b))
 
 
 # -------------------------------------------------------------- page moves
