@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     const int64_t c0 = a.cu[b];
     const int64_t nq = (int64_t)a.cu[b + 1] - c0;
     const int64_t row0 = (idx - first_tile(a, G, b)) * kRows;
-    if (c0 < 0 || nq <= 0 || c0 + nq > a.T || row0 >= nq * G) return;
+    // (rows before the first offset, and offsets that fall or pass T, are no work)
+    if (c0 < 0 || nq <= 0 || c0 + nq > a.T || row0 < 0 || row0 >= nq * G) return;
 
     // this lane's query row
     const int rows = (int)min(nq * G - row0, (int64_t)kRows);

@@ -372,3 +372,18 @@ def test_prefill_unequal_scales(w4):
     out, rel, mean = attend(x, K[0], V[0], range(n), 40, 2, 0.125)
     ok, worst = close(y[clean], out[clean], rel[clean], mean[clean], p_rounded=True)
     assert ok, worst
+
+
+def test_prefill_rows_before_the_first_offset(w4):
+    """Rows that belong to no sequence are not computed: 40 of them make a tile
+    of 128 (token, head) rows before the first sequence's own."""
+    heads, G, T, lo = 160, 4, 60, 40
+    cache, table, tl, K, V = make_cache(w4, [90], heads, 16, 16, "bf16", 46)
+    x = make_q((T, heads * G, 16), "fp32", 46)
+    y = torch.full_like(x, 7.0)
+    w4.kv_prefill_attention(x, cache, 0, table, tl, torch.tensor([lo, T], dtype=torch.int32).cuda(),
+                            out=y)
+    assert w4.w4_last_path() == "kv_prefill"
+    assert (y[:lo] == 7.0).all()
+    ok, worst = close(y[lo:], *attend(x[lo:], K[0], V[0], list(range(90 - (T - lo), 90)), 0, 0, 0.25))
+    assert ok, worst
