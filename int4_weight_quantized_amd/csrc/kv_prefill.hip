@@ -26,6 +26,19 @@
 // The maximum is only moved when a score passes it by 8 (in units of log 2):
 // weights up to 2^8 lose nothing in bf16 or fp32, and the 64 to 128
 // accumulators are rarely rescaled.
+//
+// Rounding: bf16 activations have their softmax weights rounded to bf16 once (two
+// terms: 318 us where one took 265, int8); fp32 ones are three bf16 terms, q and
+// weights alike, so that products keep 24 bits.  Sums and statistics are fp32.
+//
+// 8192 causal tokens, 32 / 8 heads of 128, bf16: 555 us, 0.99 PFLOP/s (large
+// library products in bf16: 1.21 to 1.36).  At 592 us the MFMAs were busy 42% of
+// 1.245 million cycles; a schedule with the next tile's scores beside this one's
+// exponentials took 14% fewer cycles and the same time (557 us where 559), at a
+// clock that much lower.  int8 adds the conversion of codes and the scales: 284 us
+// for ragged prompts up to 8000 with a window of 1024, 16 / 4 heads of 128.  256
+// rows a workgroup share that work among more rows, but took 274 us where 128 took
+// 265 (before the weights' sum was taken from their rounded values).
 #include "kv_attn.h"
 
 namespace w4 {
@@ -605,8 +618,8 @@ int64_t row_tiles(int64_t T, int64_t B, int64_t G) { return T * G / kRows + B; }
 
 // Few workgroups leave the chip idle and run through their tokens one tile after
 // another: their tiles are then split over up to 16 parts, as many as two
-// workgroups a CU take, and joined by a second launch (12 workgroups over 16 tiles,
-// fp32 heads of 64: 36 us in one part).
+// workgroups a CU take, and joined by a second launch (3 chunks of up to 37 tokens
+// behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 15 us split).
 int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
     const int64_t groups = row_tiles(T, B, hq / heads) * heads;
     return std::min<int64_t>(std::max<int64_t>(512 / groups, 1), 16);
