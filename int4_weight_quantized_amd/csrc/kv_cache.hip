@@ -294,7 +294,7 @@ hipError_t launch_kv_copy_pages(const KvPlanes &dst, const int32_t *dst_ids, con
 // Reference counts and tables are small next to the pages; one workgroup walks
 // them, so that ranks come from prefix sums in index order and every result is
 // the same whatever the timing.  Bound by the latency of one step after another (a
-// fork's plan 5.8 us at 300 pages and 9.2 at 6000, a compaction's 4.1 at 257 and 7.8
+// fork's plan 5.4 us at 300 pages and 8.0 at 6000, a compaction's 4.0 at 257 and 6.8
 // at 1536).
 constexpr int kPlan = 1024;
 

@@ -32,13 +32,13 @@
 // weights alike, so that products keep 24 bits.  Sums and statistics are fp32.
 //
 // 8192 causal tokens, 32 / 8 heads of 128, bf16: 555 us, 0.99 PFLOP/s (large
-// library products in bf16: 1.21 to 1.36).  At 592 us the MFMAs were busy 42% of
-// 1.245 million cycles; a schedule with the next tile's scores beside this one's
-// exponentials took 14% fewer cycles and the same time (557 us where 559), at a
-// clock that much lower.  int8 adds the conversion of codes and the scales: 284 us
-// for ragged prompts up to 8000 with a window of 1024, 16 / 4 heads of 128.  256
-// rows a workgroup share that work among more rows, but took 274 us where 128 took
-// 265 (before the weights' sum was taken from their rounded values).
+// library products in bf16: 1.21 to 1.36).  The MFMAs are busy 47% of 1.12 million
+// cycles; a schedule with the next tile's scores beside this one's exponentials
+// took 1.07 million and the same time (557 us where 559), so a lower clock.
+// int8 adds the conversion of codes and the scales: 284 us for ragged prompts up to
+// 8000 with a window of 1024, 16 / 4 heads of 128.  256 rows a workgroup share that
+// work among more rows, but took 274 us where 128 took 265 (both before the weights'
+// sum was taken from their rounded values).
 #include "kv_attn.h"
 
 namespace w4 {
