@@ -31,7 +31,7 @@
 // terms: 318 us where one took 265, int8); fp32 ones are three bf16 terms, q and
 // weights alike, so that products keep 24 bits.  Sums and statistics are fp32.
 //
-// 8192 causal tokens, 32 / 8 heads of 128, bf16: 555 us, 0.99 PFLOP/s (large
+// 8192 causal tokens, 32 / 8 heads of 128, bf16: 544 us, 1.01 PFLOP/s (large
 // library products in bf16: 1.21 to 1.36).  The MFMAs are busy 47% of 1.12 million
 // cycles; a schedule with the next tile's scores beside this one's exponentials
 // took 1.07 million and the same time (557 us where 559), so a lower clock.
@@ -443,9 +443,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[t][r]);
-        mt = fmaxf(mt, __shfl_xor(mt, 32, kWave)) * sc;
+        mt *= sc;
         if (__any(mt > m + kSlack)) {
-            const float mn = fmaxf(m, mt);
+            // (the row's other half is asked only here)
+            const float mn = fmaxf(m, fmaxf(mt, __shfl_xor(mt, 32, kWave)));
             const float alpha = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= alpha;
