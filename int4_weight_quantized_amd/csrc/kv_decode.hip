@@ -31,8 +31,8 @@
 //
 // Bound by memory.  4 sequences of 131072 tokens, 64 / 8 heads of 128, bf16: 331
 // us, 6.5 TB/s (a plain read: 7.05; this kernel's loads without its products: 325
-// us).  64 ragged sequences up to 8191, 32 / 8 heads, int8, fp32 activations: 101
-// us, 5.2 TB/s.  One token behind 700 with a window of 512, 4 / 1 heads of 256: 10.9
+// us).  64 ragged sequences up to 8191, 32 / 8 heads, int8, fp32 activations: 100
+// us, 5.3 TB/s.  One token behind 700 with a window of 512, 4 / 1 heads of 256: 10.7
 // us, launch and memory latency.
 #include "kv_attn.h"
 

@@ -31,11 +31,11 @@
 // terms: 318 us where one took 265, int8); fp32 ones are three bf16 terms, q and
 // weights alike, so that products keep 24 bits.  Sums and statistics are fp32.
 //
-// 8192 causal tokens, 32 / 8 heads of 128, bf16: 544 us, 1.01 PFLOP/s (large
-// library products in bf16: 1.21 to 1.36).  The MFMAs are busy 47% of 1.12 million
-// cycles; a schedule with the next tile's scores beside this one's exponentials
-// took 1.07 million and the same time (557 us where 559), so a lower clock.
-// int8 adds the conversion of codes and the scales: 284 us for ragged prompts up to
+// 8192 causal tokens, 32 / 8 heads of 128, bf16: 537 us, 1.02 PFLOP/s (large
+// library products in bf16: 1.21 to 1.36).  The MFMAs are busy 49% of 1.07 million
+// cycles.  A schedule with the next tile's scores beside this one's exponentials was
+// no faster (557 us where 559 without) and spilled registers for int8.
+// int8 adds the conversion of codes and the scales: 277 us for ragged prompts up to
 // 8000 with a window of 1024, 16 / 4 heads of 128.  256 rows a workgroup share that
 // work among more rows, but took 274 us where 128 took 265 (both before the weights'
 // sum was taken from their rounded values).
@@ -639,7 +639,7 @@ int64_t row_tiles(int64_t T, int64_t B, int64_t G) { return T * G / kRows + B; }
 // Few workgroups leave the chip idle and run through their tokens one tile after
 // another: their tiles are then split over up to kMaxParts parts, as many as two
 // workgroups a CU take, and joined by a second launch (3 chunks of up to 37 tokens
-// behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 14 us split).
+// behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 13 us split).
 int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
     const int64_t groups = row_tiles(T, B, hq / heads) * heads;
     return std::min<int64_t>(std::max<int64_t>(512 / groups, 1), kMaxParts);
