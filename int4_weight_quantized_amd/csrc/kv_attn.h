@@ -91,10 +91,16 @@ __device__ __forceinline__ int kv_length(const KvAttnArgs &a, int64_t b) {
     return min(max(a.lens[b], 0), (int)min(a.c.W << a.c.shift, kMaxLength));
 }
 
-// (m, l, y) += another part (mk, lk, z) of the same row.
+// (m, l, y) += another part (mk, lk, z) of the same row.  A part without a
+// maximum is empty (zeros) or has seen nothing but NaN: its sums are added as they
+// stand, so that the NaN reaches the row.
 __device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk, float lk,
                                          float4 z) {
-    if (mk == -INFINITY) return;
+    if (mk == -INFINITY) {
+        l += lk;
+        y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+        return;
+    }
     const float mn = fmaxf(m, mk);
     const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
     const float fb = __builtin_amdgcn_exp2f(mk - mn);

@@ -539,7 +539,9 @@ __global__ __launch_bounds__(
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const float mw = sm[w * 16 + r];
-                lr += mw == -INFINITY ? 0.0f : sl[w * 16 + r] * __builtin_amdgcn_exp2f(mw - mr);
+                // (no maximum: nothing seen, l = 0, or nothing but NaN, l = NaN)
+                lr += mw == -INFINITY ? sl[w * 16 + r]
+                                      : sl[w * 16 + r] * __builtin_amdgcn_exp2f(mw - mr);
                 const float4 z =
                     *reinterpret_cast<const float4 *>(join + (w * hd.rows + r) * kRow + d);
                 y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;

@@ -613,12 +613,12 @@ __global__ __launch_bounds__(256) void k_kv_prefill_join(KvAttnArgs a, int parts
         for (int x = 0; x < kEach; ++x) {
             const int i = grp + x * kGroups;
             const float *p = RowOut{row, min(i, parts - 1), parts}.sums(a);
-            mk[x] = i < parts ? p[D] : -INFINITY;
-            lk[x] = p[D + 1];
+            mk[x] = p[D], lk[x] = p[D + 1];
             z[x] = *reinterpret_cast<const float4 *>(p + d);
         }
 #pragma unroll
-        for (int x = 0; x < kEach; ++x) add_part(m, l, y, mk[x], lk[x], z[x]);
+        for (int x = 0; x < kEach; ++x)
+            if (grp + x * kGroups < parts) add_part(m, l, y, mk[x], lk[x], z[x]);
     }
     so[tid] = y, sm[tid] = m, sl[tid] = l;
     __syncthreads();
