@@ -96,14 +96,9 @@ __device__ __forceinline__ int kv_length(const KvAttnArgs &a, int64_t b) {
 // stand, so that the NaN reaches the row.
 __device__ __forceinline__ void add_part(float &m, float &l, float4 &y, float mk, float lk,
                                          float4 z) {
-    if (mk == -INFINITY) {
-        l += lk;
-        y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-        return;
-    }
     const float mn = fmaxf(m, mk);
     const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
-    const float fb = __builtin_amdgcn_exp2f(mk - mn);
+    const float fb = mk == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mk - mn);
     m = mn;
     l = l * fa + lk * fb;
     y.x = y.x * fa + z.x * fb;

@@ -503,12 +503,14 @@ __global__ __launch_bounds__(
         // join the waves: a common maximum, then the sum of the rescaled parts
         l += __shfl_xor(l, 16, kWave);
         l += __shfl_xor(l, 32, kWave);
-        if (g == 0) sm[wave * 16 + c] = m, sl[wave * 16 + c] = l;
+        if (g == 0) sm[wave * 16 + c] = m;
         __syncthreads();
         float mx = sm[c];
 #pragma unroll
         for (int w = 1; w < NW; ++w) mx = fmaxf(mx, sm[w * 16 + c]);
-        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
+        // (no maximum: the wave has seen nothing, its sums are zeros, or nothing but NaN)
+        const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);
+        if (g == 0) sl[wave * 16 + c] = l * f;
         if constexpr (PACK) {
 #pragma unroll
             for (int e = 0; e < VD; ++e)
@@ -529,7 +531,9 @@ __global__ __launch_bounds__(
         if (SPLIT && u0 == 0 && u1 < units) mark = KvSplitPair{b, cur.h, mark.flags | kStarts};
         if (SPLIT && u0 > 0 && u1 == units) mark.flags |= kEnds;
         const KvPartial part_ws(a, hd, DP, (int64_t)blockIdx.x * 2 + (u0 == 0));
-        for (int at = threadIdx.x; at < rows * (DP / 4); at += NW * 64) {
+        int first = threadIdx.x;  // (opaque: its addresses stay out of the loop's registers)
+        asm volatile("" : "+v"(first));
+        for (int at = first; at < rows * (DP / 4); at += NW * 64) {
             const int r = at / (DP / 4), d = at % (DP / 4) * 4;
             float mr = sm[r];
 #pragma unroll
@@ -538,10 +542,7 @@ __global__ __launch_bounds__(
             float4 y = {};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float mw = sm[w * 16 + r];
-                // (no maximum: nothing seen, l = 0, or nothing but NaN, l = NaN)
-                lr += mw == -INFINITY ? sl[w * 16 + r]
-                                      : sl[w * 16 + r] * __builtin_amdgcn_exp2f(mw - mr);
+                lr += sl[w * 16 + r];
                 const float4 z =
                     *reinterpret_cast<const float4 *>(join + (w * hd.rows + r) * kRow + d);
                 y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
