@@ -404,10 +404,11 @@ typedef struct {
 typedef enum { KV_X_BF16 = 0, KV_X_FP32 = 1 } kv_x_dtype;
 
 /* Write new tokens' K and V into `layer`.  Sequence b's tokens are rows
- * cu[b] .. cu[b + 1] - 1 of k and v (cu [B + 1] int32, cu[0] = 0, cu[B] = T,
- * not falling; NULL: row b is sequence b's one token, T = B) and go to
- * positions start[b], start[b] + 1, ...  A negative start[b], a position
- * beyond the row and a token without a page are skipped.
+ * cu[b] .. cu[b + 1] - 1 of k and v (cu [B + 1] int32, 0 <= cu[0] <= ... <=
+ * cu[B] <= T; NULL: row b is sequence b's one token, T = B) and go to
+ * positions start[b], start[b] + 1, ...  Rows before cu[0] and from cu[B] on
+ * belong to no sequence; they, a negative start[b], a position beyond the row
+ * and a token without a page are skipped.
  *   k, v    T rows of [heads][head_dim] values of x_dtype, k_stride / v_stride
  *           elements from one row to the next (at least heads * head_dim).
  *   KV_BF16: fp32 values are rounded to bf16 (half to even); KV_INT8: see above.
@@ -419,7 +420,7 @@ int kv_append(const kv_cache *cache, int64_t layer, const void *k, const void *v
 
 /* The reverse: the cached values of the same tokens, as fp32 or bf16
  * [T][heads][head_dim] (int8: fl(code * scale), then rounded for bf16; zeros
- * for tokens without a page). */
+ * for tokens without a page and rows of no sequence). */
 int kv_gather(const kv_cache *cache, int64_t layer, void *k, void *v, int x_dtype, int64_t T,
               int64_t B, const int32_t *table, int64_t W, const int32_t *start,
               const int32_t *cu, void *stream);
@@ -455,7 +456,7 @@ int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int
  * cu[b] .. cu[b + 1] - 1 of q (cu as in kv_append, required), the last tokens
  * of its lens[b] cached ones: the query of row cu[b] + t has position
  * pos = lens[b] - (cu[b + 1] - cu[b]) + t; one with a negative position sees
- * nothing.  Everything else as kv_decode_attention; with bf16 activations the
+ * nothing.  Rows of no sequence keep what their outputs held.  Everything else as kv_decode_attention; with bf16 activations the
  * softmax weights are rounded to bf16 for the product with V. */
 int kv_prefill_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,
                          int64_t q_stride, int64_t T, int64_t B, int64_t q_heads,

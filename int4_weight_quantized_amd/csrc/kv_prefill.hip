@@ -591,7 +591,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
 
 // Joins the parts of every row: D / 4 lanes have a row's values, 4 each, and 4
 // groups of them take a quarter of the parts each, all loads at once (the time is
-// one trip to memory: 3.8 us for 16 parts, 4.8 with four trips), joined in a fixed
+// one trip to memory: 3.9 us for 16 parts, 4.8 with four trips), joined in a fixed
 // order through LDS.
 template <bool FP32>
 __global__ __launch_bounds__(256) void k_kv_prefill_join(KvAttnArgs a, int parts) {
@@ -600,26 +600,32 @@ __global__ __launch_bounds__(256) void k_kv_prefill_join(KvAttnArgs a, int parts
     __shared__ float sm[256], sl[256];
     const int tid = threadIdx.x;
     const int D = a.c.D, lanes = D / 4, rows = 256 / (kGroups * lanes);
-    const int64_t row = (int64_t)blockIdx.x * rows + tid / (kGroups * lanes);
+    const int64_t row = (int64_t)blockIdx.x * rows + tid / (kGroups * lanes), all = a.T * a.hq;
     const int grp = tid / lanes % kGroups, d = tid % lanes * 4;
-    const bool on = tid < rows * kGroups * lanes && row < a.T * a.hq;
+    constexpr int kEach = kMaxParts / kGroups;
+    float mk[kEach], lk[kEach];
+    float4 z[kEach];
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+        const int i = grp + x * kGroups;
+        const float *p = RowOut{min(row, all - 1), min(i, parts - 1), parts}.sums(a);
+        mk[x] = p[D], lk[x] = p[D + 1];
+        z[x] = *reinterpret_cast<const float4 *>(p + d);
+    }
+    // (while they are in flight) the row's sequence: nobody wrote the parts of a row
+    // that belongs to none, and its output is left as it is
+    const int64_t token = row / a.hq;
+    const int64_t first = (int64_t)blockIdx.x * rows + tid / kWave * kWave / (kGroups * lanes);
+    int64_t b = find_sequence(a.cu, a.B, min(first, all - 1) / a.hq);
+    while (b + 1 < a.B && a.cu[b + 1] <= token) ++b;
+    const int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
+    const bool on = tid < rows * kGroups * lanes && row < all && c0 >= 0 && c1 <= a.T &&
+                    token >= c0 && token < c1;
     float m = -INFINITY, l = 0.0f;
     float4 y = {};
-    if (on) {
-        constexpr int kEach = kMaxParts / kGroups;
-        float mk[kEach], lk[kEach];
-        float4 z[kEach];
 #pragma unroll
-        for (int x = 0; x < kEach; ++x) {
-            const int i = grp + x * kGroups;
-            const float *p = RowOut{row, min(i, parts - 1), parts}.sums(a);
-            mk[x] = p[D], lk[x] = p[D + 1];
-            z[x] = *reinterpret_cast<const float4 *>(p + d);
-        }
-#pragma unroll
-        for (int x = 0; x < kEach; ++x)
-            if (grp + x * kGroups < parts) add_part(m, l, y, mk[x], lk[x], z[x]);
-    }
+    for (int x = 0; x < kEach; ++x)
+        if (grp + x * kGroups < parts) add_part(m, l, y, mk[x], lk[x], z[x]);
     so[tid] = y, sm[tid] = m, sl[tid] = l;
     __syncthreads();
     if (!on || grp) return;
