@@ -426,7 +426,9 @@ int kv_gather(const kv_cache *cache, int64_t layer, void *k, void *v, int x_dtyp
               const int32_t *cu, void *stream);
 
 /* Bytes of device workspace of kv_decode_attention (rows = B) and
- * kv_prefill_attention (rows = T); 0 for invalid sizes. */
+ * kv_prefill_attention (rows = T); 0 for invalid sizes.  It does not fall when
+ * rows or B grow: the workspace of a program's largest call serves its smaller
+ * ones. */
 size_t kv_attention_workspace_bytes(int64_t rows, int64_t B, int64_t q_heads, int64_t heads,
                                     int64_t head_dim);
 

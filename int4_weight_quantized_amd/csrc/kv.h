@@ -58,7 +58,7 @@ struct KvAttnArgs {
     void *ws;
 };
 
-size_t kv_attn_ws_bytes(int64_t rows, int64_t B, int64_t hq, int64_t heads, int64_t D);
+size_t kv_attn_ws_bytes(int64_t rows, int64_t hq, int64_t heads, int64_t D);
 // `path`: the kernel variant taken.
 hipError_t launch_kv_attention(const KvAttnArgs &a, const char **path, hipStream_t st);
 

@@ -196,7 +196,7 @@ size_t kv_attention_workspace_bytes(int64_t rows, int64_t B, int64_t q_heads, in
         head_dim % 16 != 0 || q_heads % heads != 0 || q_heads > 65535 ||
         rows > kMaxRows || rows > kMaxQueries / q_heads || B > kMaxPairs / q_heads)
         return 0;
-    return w4::kv_attn_ws_bytes(rows, B, q_heads, heads, head_dim);
+    return w4::kv_attn_ws_bytes(rows, q_heads, heads, head_dim);
 }
 
 int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,

@@ -9,7 +9,7 @@ namespace w4 {
 
 size_t kv_decode_ws_bytes(int64_t hq, int64_t heads, int64_t D);
 hipError_t launch_kv_decode(const KvAttnArgs &a, const char **path, hipStream_t st);
-size_t kv_prefill_ws_bytes(int64_t T, int64_t B, int64_t hq, int64_t heads, int64_t D);
+size_t kv_prefill_ws_bytes(int64_t T, int64_t hq, int64_t heads, int64_t D);
 hipError_t launch_kv_prefill(const KvAttnArgs &a, const char **path, hipStream_t st);
 
 // Two int8 codes as a bf16 pair: 8 bits are exact in bf16, so the upper halves

@@ -3,8 +3,8 @@
 
 namespace w4 {
 
-size_t kv_attn_ws_bytes(int64_t rows, int64_t B, int64_t hq, int64_t heads, int64_t D) {
-    return std::max(kv_decode_ws_bytes(hq, heads, D), kv_prefill_ws_bytes(rows, B, hq, heads, D));
+size_t kv_attn_ws_bytes(int64_t rows, int64_t hq, int64_t heads, int64_t D) {
+    return std::max(kv_decode_ws_bytes(hq, heads, D), kv_prefill_ws_bytes(rows, hq, heads, D));
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, const char **path, hipStream_t st) {

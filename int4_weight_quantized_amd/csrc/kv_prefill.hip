@@ -646,9 +646,10 @@ int64_t row_tiles(int64_t T, int64_t B, int64_t G) { return T * G / kRows + B; }
 // another: their tiles are then split over up to kMaxParts parts, as many as two
 // workgroups a CU take, and joined by a second launch (3 chunks of up to 37 tokens
 // behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 13 us split).
+constexpr int64_t kPartBlocks = 512;
 int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
     const int64_t groups = row_tiles(T, B, hq / heads) * heads;
-    return std::min<int64_t>(std::max<int64_t>(512 / groups, 1), kMaxParts);
+    return std::min<int64_t>(std::max<int64_t>(kPartBlocks / groups, 1), kMaxParts);
 }
 
 template <int DP, bool INT8, bool FP32>
@@ -680,9 +681,17 @@ hipError_t launch_types(const KvAttnArgs &a, const char **path, hipStream_t st) 
 
 }  // namespace
 
-size_t kv_prefill_ws_bytes(int64_t T, int64_t B, int64_t hq, int64_t heads, int64_t D) {
-    const int64_t parts = most_parts(T, B, hq, heads);
-    return parts > 1 ? (size_t)(T * hq * parts * (D + 4) * 4) : 0;
+// Bytes of the parts of every call of up to T tokens.  A larger call has fewer
+// parts, so the most comes from the largest calls that still have p of them: those
+// of one sequence whose workgroups are at most 512 / p.
+size_t kv_prefill_ws_bytes(int64_t T, int64_t hq, int64_t heads, int64_t D) {
+    int64_t rows = 0;
+    for (int64_t p = 2; p <= kMaxParts; ++p) {
+        const int64_t tiles = kPartBlocks / p / heads;  // T' * G / kRows + 1 at most
+        if (tiles > 0)
+            rows = std::max(rows, std::min(T, (tiles * kRows - 1) / (hq / heads)) * hq * p);
+    }
+    return (size_t)(rows * (D + 4) * 4);
 }
 
 hipError_t launch_kv_prefill(const KvAttnArgs &a, const char **path, hipStream_t st) {

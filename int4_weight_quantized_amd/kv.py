@@ -208,7 +208,8 @@ def kv_gather(cache: KVCache, layer: int, table: torch.Tensor, start: torch.Tens
 
 def kv_attention_workspace_bytes(rows: int, B: int, q_heads: int, heads: int,
                                  head_dim: int) -> int:
-    """Workspace of the attention calls (rows: query tokens of the call)."""
+    """Workspace of the attention calls (rows: query tokens of the call); it
+    serves every call of up to `rows` rows and B sequences."""
     return int(lib().kv_attention_workspace_bytes(rows, B, q_heads, heads, head_dim))
 
 
