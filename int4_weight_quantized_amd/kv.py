@@ -130,6 +130,21 @@ def _table(table: torch.Tensor, rows, dev):
     return _ptr(table, "table", torch.int32, (n if rows is None else rows, W), dev), n, W
 
 
+def _table_device(table: torch.Tensor):
+    """The device of a call that has no cache: its table's, which must be a GPU."""
+    if not isinstance(table, torch.Tensor):
+        raise TypeError("table must be a tensor")
+    if not table.is_cuda:
+        raise ValueError("table must be a GPU tensor")
+    return table.device
+
+
+def _count(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.numel()
+
+
 def _rows(x: torch.Tensor, name: str, heads, head_dim: int, dev, dtype=None):
     """(pointer, row stride) of [tokens, heads, head_dim] values whose rows may
     lie apart (slices of a joint projection's output)."""
@@ -228,8 +243,8 @@ def _attention(name, q, cache, layer, table, lens, cu, scale, window, sinks, out
         workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
     rest = (1.0 / math.sqrt(D) if scale is None else scale, window, sinks,
             _ptr(out, "out", q.dtype, (T, hq, D), dev),
-            _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),
-            _stream(stream, dev))
+            _ptr(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev),
+            workspace.numel(), _stream(stream, dev))
     if cu is None:
         rc = lib().kv_decode_attention(c._ref, layer, pq, _XTYPES[q.dtype], ldq, T, hq, pt, W,
                                        _int32(lens, "lens", B, dev), *rest)
@@ -271,7 +286,7 @@ def kv_copy_pages(dst: KVCache, dst_ids: torch.Tensor, src: KVCache, src_ids: to
     d, s = _cache(dst), _cache(src)
     if d.device != s.device:
         raise ValueError(f"dst is on {d.device}, src on {s.device}")
-    n = dst_ids.numel()
+    n = _count(dst_ids, "dst_ids")
     _check("kv_copy_pages", lib().kv_copy_pages(
         d._ref, _int32(dst_ids, "dst_ids", n, d.device), s._ref,
         _int32(src_ids, "src_ids", n, d.device), n, _stream(stream, d.device)))
@@ -281,20 +296,22 @@ def _work(workspace, need, dev, stream, kept=None):
     if workspace is None:
         workspace = (kept if kept is not None and kept.numel() >= need
                      else _empty((need,), torch.uint8, dev, stream))
-    return workspace, _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
+    at = _ptr(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
+    return workspace, at, workspace.numel()
 
 
 def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, add: torch.Tensor,
                page_size: int, ok=None, workspace=None, stream=None) -> torch.Tensor:
     """Pages for add[s] more tokens of every slot, from the free ones (refs 0)
     in ascending order; ok [S]: 1 where the slot has them."""
-    dev = table.device
+    dev = _table_device(table)
     pt, S, W = _table(table, None, dev)
+    pages = _count(refs, "refs")
     ok = _empty((S,), torch.int32, dev, stream) if ok is None else ok
     work, *ws = _work(workspace, 8 * S + 256, dev, stream)  # (work lives to the end of the call)
     _check("kv_reserve", lib().kv_reserve(
-        pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", refs.numel(), dev),
-        refs.numel(), page_size, _int32(add, "add", S, dev), _int32(ok, "ok", S, dev),
+        pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", pages, dev),
+        pages, page_size, _int32(add, "add", S, dev), _int32(ok, "ok", S, dev),
         *ws, _stream(stream, dev)))
     return ok
 
@@ -307,7 +324,7 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
     c = _cache(cache)
     dev = c.device
     pt, S, W = _table(table, None, dev)
-    n = parents.numel()
+    n = _count(parents, "parents")
     ok = _empty((n,), torch.int32, dev, stream) if ok is None else ok
     work, *ws = _work(workspace, 16 * n + 256, dev, stream, c._moves)
     _check("kv_fork", lib().kv_fork(
@@ -321,12 +338,12 @@ def kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, slots: 
             stream=None) -> None:
     """Retire slots: their pages lose a reference, their rows become -1, their
     lengths 0."""
-    dev = table.device
+    dev = _table_device(table)
     pt, S, W = _table(table, None, dev)
-    n = slots.numel()
+    n, pages = _count(slots, "slots"), _count(refs, "refs")
     _check("kv_free", lib().kv_free(
-        pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", refs.numel(), dev),
-        refs.numel(), _int32(slots, "slots", n, dev), n, _stream(stream, dev)))
+        pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", pages, dev),
+        pages, _int32(slots, "slots", n, dev), n, _stream(stream, dev)))
 
 
 def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor, table_out=None,
