@@ -101,9 +101,6 @@ class KVCache:
                          _opt(v_scale, "v_scale", torch.float32, shape[:4], dev), *shape,
                          KV_INT8 if int8 else KV_BF16)
         self._ref = ctypes.addressof(self._c)
-        # workspace of the page moves (calls that move this cache's pages are in
-        # order anyway: they write the same pages, tables and counts)
-        self._moves = torch.empty((16 * self.pages + 256,), dtype=torch.uint8, device=dev)
 
     @classmethod
     def empty(cls, layers: int, pages: int, heads: int, page_size: int, head_dim: int,
@@ -179,6 +176,14 @@ def _empty(shape, dtype, dev, stream):
 
 def _int32(t, name, n, dev):
     return _ptr(t, name, torch.int32, (n,), dev)
+
+
+def _int32_out(t, name, n, dev, stream):
+    """The caller's output, checked, or a new one, and its pointer."""
+    if t is None:
+        t = _empty(n, torch.int32, dev, stream)
+        return t, t.data_ptr()
+    return t, _int32(t, name, n, dev)
 
 
 def kv_append(cache: KVCache, layer: int, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -292,10 +297,12 @@ def kv_copy_pages(dst: KVCache, dst_ids: torch.Tensor, src: KVCache, src_ids: to
         _int32(src_ids, "src_ids", n, d.device), n, _stream(stream, d.device)))
 
 
-def _work(workspace, need, dev, stream, kept=None):
+def _work(workspace, need, dev, stream):
+    """The workspace, its pointer and its size; without one, memory of the call's
+    own stream (kept with the cache it could end, or be used, before the call ran)."""
     if workspace is None:
-        workspace = (kept if kept is not None and kept.numel() >= need
-                     else _empty((need,), torch.uint8, dev, stream))
+        workspace = _empty(need, torch.uint8, dev, stream)
+        return workspace, workspace.data_ptr(), need
     at = _ptr(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
     return workspace, at, workspace.numel()
 
@@ -307,11 +314,11 @@ def kv_reserve(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, add:
     dev = _table_device(table)
     pt, S, W = _table(table, None, dev)
     pages = _count(refs, "refs")
-    ok = _empty((S,), torch.int32, dev, stream) if ok is None else ok
+    ok, to = _int32_out(ok, "ok", S, dev, stream)
     work, *ws = _work(workspace, 8 * S + 256, dev, stream)  # (work lives to the end of the call)
     _check("kv_reserve", lib().kv_reserve(
         pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", pages, dev),
-        pages, page_size, _int32(add, "add", S, dev), _int32(ok, "ok", S, dev),
+        pages, page_size, _int32(add, "add", S, dev), to,
         *ws, _stream(stream, dev)))
     return ok
 
@@ -325,12 +332,12 @@ def kv_fork(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, refs: torch
     dev = c.device
     pt, S, W = _table(table, None, dev)
     n = _count(parents, "parents")
-    ok = _empty((n,), torch.int32, dev, stream) if ok is None else ok
-    work, *ws = _work(workspace, 16 * n + 256, dev, stream, c._moves)
+    ok, to = _int32_out(ok, "ok", n, dev, stream)
+    work, *ws = _work(workspace, 16 * n + 256, dev, stream)
     _check("kv_fork", lib().kv_fork(
         c._ref, pt, S, W, _int32(lens, "lens", S, dev), _int32(refs, "refs", c.pages, dev),
         _int32(parents, "parents", n, dev), _int32(children, "children", n, dev), n,
-        _int32(ok, "ok", n, dev), *ws, _stream(stream, dev)))
+        to, *ws, _stream(stream, dev)))
     return ok
 
 
@@ -356,11 +363,11 @@ def kv_compact(cache: KVCache, table: torch.Tensor, refs: torch.Tensor, table_ou
     pt, S, W = _table(table, None, dev)
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
-    live = _empty((1,), torch.int32, dev, stream) if live is None else live
-    work, *ws = _work(workspace, 8 * c.pages + 256, dev, stream, c._moves)
+    live, count = _int32_out(live, "live", 1, dev, stream)
+    work, *ws = _work(workspace, 8 * c.pages + 256, dev, stream)
     _check("kv_compact", lib().kv_compact(
         c._ref, pt, S, W, _int32(refs, "refs", c.pages, dev),
         _ptr(table_out, "table_out", torch.int32, (S, W), dev),
-        _int32(refs_out, "refs_out", c.pages, dev), _int32(live, "live", 1, dev),
+        _int32(refs_out, "refs_out", c.pages, dev), count,
         *ws, _stream(stream, dev)))
     return table_out, refs_out, live

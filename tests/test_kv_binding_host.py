@@ -43,3 +43,44 @@ def test_what_is_no_tensor_is_named(no_library, bad):
         kv._count(bad, "refs")
     with pytest.raises(TypeError, match="workspace must be a tensor"):
         kv._work(bad if bad is not None else 0, 16, c.device, None)
+
+
+class Calls:
+    """Stands in for the library: keeps each call's arguments."""
+
+    def __init__(self):
+        self.seen = []
+
+    def __call__(self):
+        return self
+
+    def __getattr__(self, name):
+        return lambda *a: self.seen.append((name, a)) or 0
+
+
+@pytest.mark.parametrize("stream", [None, 77])
+def test_page_moves_use_workspaces_of_the_call_s_stream(monkeypatch, stream):
+    """The lists of a fork or a compaction lie in memory of the stream that runs
+    it, not in memory that ends with the cache object or belongs to another stream."""
+    made = {}
+
+    def empty(shape, dtype, dev, on):
+        t = torch.empty(shape, dtype=dtype)
+        made[t.data_ptr()] = on
+        keep.append(t)
+        return t
+
+    keep, calls = [], Calls()
+    monkeypatch.setattr(kv, "_empty", empty)
+    monkeypatch.setattr(kv, "lib", calls)
+    monkeypatch.setattr(kv, "_stream", lambda s, dev: 0 if s is None else s)
+    c = object.__new__(w4.KVCache)
+    c.device, c.pages, c._ref = torch.device("cpu"), 10, 0
+    c._moves = torch.empty(1000, dtype=torch.uint8)
+    w4.kv_fork(c, ints(3, 4), ints(3), ints(10), ints(2), ints(2), stream=stream)
+    w4.kv_compact(c, ints(3, 4), ints(10), stream=stream)
+    assert [n for n, _ in calls.seen] == ["kv_fork", "kv_compact"]
+    for name, a in calls.seen:
+        ws, size, on = a[-3:]
+        assert on == (stream or 0)
+        assert made[ws] == stream and size == 256 + (16 * 2 if name == "kv_fork" else 8 * 10)
