@@ -372,7 +372,9 @@ int w4a8_linear_prepacked(const float *X, int64_t M, int64_t K, int64_t N,
  *            each token and head (KV_INT8; NULL for KV_BF16): the value is
  *            code * scale, scale = fl(max_d |x[d]| * fl(1 / 127)) of the head's
  *            vector, code = clamp(rne(fl(x / scale)), -128, 127) (0 where the
- *            scale is 0): a8_quantize_act's rule but for the scale's last bit;
+ *            scale is 0): a8_quantize_act's rule but for the scale's last bit.  A
+ *            vector with a NaN or an infinity in it gets the scale NaN: all of it
+ *            is read back, and attended, as NaN;
  *   table    [S][W] int32: entry j of a row is the page of tokens
  *            j * page_size ... (j + 1) * page_size - 1, -1 where there is none;
  *   lens     [S] int32, cached tokens; refs [pages] int32, how many rows hold

@@ -79,7 +79,8 @@ __device__ __forceinline__ void load8(const void *x, int64_t at, bool vec, float
 
 // Rounding to the cache's type happens once, here: bf16 half to even, or int8 with
 // the scale absmax * fl(1 / 127) of the head's vector (one multiplication, within
-// one unit in the last place of the quotient) and codes rne(fl(x / scale)).
+// one unit in the last place of the quotient) and codes rne(fl(x / scale)).  A
+// vector with a value that is not finite has no int8 form: its scale is NaN.
 template <bool INT8, bool FP32, int LPV>
 __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const void *k,
                                                    const void *v, int64_t ldk, int64_t ldv,
@@ -97,13 +98,14 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
     const bool on = p.vec >= 0 && d < c.D;
     uint8_t *pool = isv ? c.v : c.k;
     if constexpr (INT8) {
-        float m = 0.0f;
+        // the bits of |x| order as the values do, infinity and NaN above them all
+        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = LPV / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+        for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
         if (!on) return;
-        const float s = m * (1.0f / 127.0f);
+        const float s = m < 0x7F800000u ? __uint_as_float(m) * (1.0f / 127.0f) : NAN;
         uint32_t w[2] = {};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
