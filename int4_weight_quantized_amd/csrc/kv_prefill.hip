@@ -18,7 +18,9 @@
 // read ds_read_b64_tr_b16 (16 lanes read 4 rows of 16 values and get a column's
 // 4 each).  A bf16 cache goes to LDS directly (no registers, the swizzle is in
 // each lane's global address), int8 codes through registers, where they become
-// bf16 (exact); their scales multiply the scores and the softmax weights.  Two
+// bf16 (exact); their scales multiply the scores and the softmax weights (a
+// workgroup that meets a scale of V outside 2^-80 to 2^80 takes its rows token by
+// token instead, see plain_row).  Two
 // LDS buffers, the next tile's loads in flight during this one's products, one
 // barrier a tile; a wave loads the 16 tokens of one quarter, so that it needs
 // one page.
@@ -51,6 +53,10 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kRows = 128, kTile = 64, kThreads = 256;
 constexpr float kSlack = 8.0f;
+// Scales of V that the products take: the weights times them, and their reciprocals,
+// stay far from the ends of the exponent's range (a weight of 2^-46 times the least
+// one is still a normal number).
+constexpr float kScaleMin = 0x1p-80f, kScaleMax = 0x1p80f;
 
 __device__ __forceinline__ v16f mfma32(uint4 a, uint4 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
@@ -111,11 +117,12 @@ struct RowOut {
 };
 
 // One query row without the matrix cores, token by token, so that a token the
-// row does not see takes no part at all: for workgroups whose edge tiles hold
-// infinities or NaN in V (the products of a tile would carry them to every
-// row as 0 * inf).  bf16 cache; the whole workgroup, `buf` 516 floats of LDS;
+// row does not see takes no part at all and a value is code * scale whatever the
+// scale: for workgroups whose edge tiles hold infinities or NaN in V (the products
+// of a tile would carry them to every row as 0 * inf), or whose tiles hold scales of
+// V outside kScaleMin to kScaleMax.  The whole workgroup, `buf` 516 floats of LDS;
 // tile_token(i) is the first token of tile i, i from i0 to i1 - 1.
-template <bool FP32, class F>
+template <bool INT8, bool FP32, class F>
 __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t token, int h, int kvh,
                           int pos, F tile_token, int i0, int i1, RowOut out, float *buf) {
     float *q = buf, *p = buf + 256;
@@ -127,8 +134,12 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
         q[tid] = FP32 ? reinterpret_cast<const float *>(a.q)[at]
                       : bf16_lo(reinterpret_cast<const uint16_t *>(a.q)[at]);
     }
-    const uint16_t *ck = reinterpret_cast<const uint16_t *>(a.c.k);
-    const uint16_t *cv = reinterpret_cast<const uint16_t *>(a.c.v);
+    auto value = [&](const uint8_t *pool, const float *scales, int64_t vec, int d) {
+        if constexpr (INT8)
+            return (float)(int8_t)pool[vec * D + d] * scales[vec];
+        else
+            return bf16_lo(reinterpret_cast<const uint16_t *>(pool)[vec * D + d]);
+    };
     auto vector = [&](int t) {
         const int pg = kv_page(a.c, table, t);
         return pg < 0 ? (int64_t)-1 : kv_vector(a.c, pg, kvh, t);
@@ -143,7 +154,7 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
             float s = -INFINITY;
             if (vec >= 0) {
                 float x = 0.0f;
-                for (int d = 0; d < D; ++d) x = __builtin_fmaf(q[d], bf16_lo(ck[vec * D + d]), x);
+                for (int d = 0; d < D; ++d) x = __builtin_fmaf(q[d], value(a.c.k, a.c.ks, vec, d), x);
                 s = x * a.scale * 1.44269504088896340736f;
             }
             const float mn = fmaxf(m, wave_max(s));
@@ -160,7 +171,7 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
             if (p[j] < 0.0f) continue;
             l += p[j];
             const int64_t vj = vector(t0 + j);
-            if (tid < D) o = __builtin_fmaf(p[j], bf16_lo(cv[vj * D + tid]), o);
+            if (tid < D) o = __builtin_fmaf(p[j], value(a.c.v, a.c.vs, vj, tid), o);
         }
     }
     if (out.parts > 1) {
@@ -189,7 +200,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ float sks[2][kTile], svs[2][kTile];
     __shared__ __align__(8) uint16_t inv_hi[2][kTile], inv_lo[2][kTile];  // 1 / svs, two bf16 terms
-    __shared__ int odd;  // whether a tile at an edge has values of V that are not finite
+    __shared__ int odd;  // whether a tile has values or scales of V that the products cannot take
 
     const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -306,6 +317,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
     auto finish = [&](int i, int buf, bool edge) {
         uint8_t *kb = lds + buf * kBuf + wave * 16 * kPitch, *vb = kb + kVTile;
         if constexpr (INT8) {
+            // the sum of bf16 weights divides the scales out again: a scale of zero is
+            // taken as codes of zero
+            const uint64_t zero = FP32 ? 0 : __ballot(vs == 0.0f);  // (lane % 16: the token)
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j)
+                    if (zero >> (j * kRowsPer + lane / kCode) & 1) stage[kLoads + j] = u32x4{};
+            }
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int t = j * kRowsPer + lane / kCode, ch = lane % kCode * 2;
@@ -320,12 +339,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 }
             }
             if (lane < 16) {
-                const int at = wave * 16 + lane;
+                const int at = wave * 16 + lane, t = tile_token(i) + at;
                 sks[buf][at] = ks;
-                // (finite, so that an unseen token's weight of zero stays zero, and not
-                // zero, so that it can be divided by: codes times 2^-100 count nothing)
-                float v = fminf(vs, 3.0e38f);
-                if (fabsf(v) < 0x1p-100f) v = 0x1p-100f;
+                const bool fits = fabsf(vs) >= kScaleMin && fabsf(vs) <= kScaleMax;
+                // (not finite or far off: what a row sees, plain_row takes as it is; an
+                // unseen token's weight of zero stays zero)
+                if (!fits && vs != 0.0f && t <= pos1 && (t >= low0 || t < a.sinks) &&
+                    !(gone_of(i) >> wave & 1))
+                    odd = 1;
+                const float v = fits || (FP32 && vs == 0.0f) ? vs : 1.0f;
                 svs[buf][at] = v;
                 if constexpr (!FP32) {
                     const float inv = 1.0f / v;
@@ -532,11 +554,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
         lds_barrier();
     }
 
-    if (!INT8 && odd) {
+    if (odd) {
         for (int i = 0; i < rows; ++i) {
             const int64_t rr = row0 + i;
             const int tk = (int)(rr / G), h = kvh * G + (int)(rr - (int64_t)tk * G);
-            plain_row<FP32>(a, table, c0 + tk, h, kvh, len - (int)nq + tk, tile_token, i0, i1,
+            plain_row<INT8, FP32>(a, table, c0 + tk, h, kvh, len - (int)nq + tk, tile_token, i0, i1,
                             RowOut{(c0 + tk) * a.hq + h, part, parts},
                             reinterpret_cast<float *>(lds));
         }
