@@ -345,6 +345,10 @@ __global__ __launch_bounds__(
         }
         v4f o[VD] = {};
         float m = -INFINITY, l = 0.0f;
+        // int8: weights are 2^shift times as large where the wave's first scales of V
+        // are tiny, so that the terms of their products stay normal numbers
+        float shift = 0.0f;
+        bool fresh = true;
         const int32_t *table = a.c.table + b * a.c.W;
         const int last = min(u1 * NW, sp.tiles);
         auto tile_token = [&](int i) {
@@ -448,6 +452,17 @@ __global__ __launch_bounds__(
                         }
                     }
             }
+            if (INT8 && fresh) {
+                float big = 0.0f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(t.vs[h][r]));
+                big = fmaxf(big, __shfl_xor(big, 16, kWave));
+                big = fmaxf(big, __shfl_xor(big, 32, kWave));
+                shift = __builtin_amdgcn_readfirstlane(big < 0x1p-60f) ? 40.0f : 0.0f;
+                fresh = false;
+            }
             float mt = x[0][0];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -465,7 +480,7 @@ __global__ __launch_bounds__(
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[e][r] *= alpha;
             }
-            const float mu = m == -INFINITY ? 0.0f : m;
+            const float mu = m == -INFINITY ? 0.0f : m - shift;
             float p[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -500,6 +515,7 @@ __global__ __launch_bounds__(
             }
         }
 
+        m -= shift;  // (what the weights are relative to)
         // join the waves: a common maximum, then the sum of the rescaled parts
         l += __shfl_xor(l, 16, kWave);
         l += __shfl_xor(l, 32, kWave);
