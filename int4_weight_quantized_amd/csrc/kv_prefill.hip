@@ -19,7 +19,7 @@
 // 4 each).  A bf16 cache goes to LDS directly (no registers, the swizzle is in
 // each lane's global address), int8 codes through registers, where they become
 // bf16 (exact); their scales multiply the scores and the softmax weights (a
-// workgroup that meets a scale of V outside 2^-80 to 2^80 takes its rows token by
+// workgroup that meets a scale of V outside 2^-110 to 2^50 takes its rows token by
 // token instead, see plain_row).  Two
 // LDS buffers, the next tile's loads in flight during this one's products, one
 // barrier a tile; a wave loads the 16 tokens of one quarter, so that it needs
@@ -53,10 +53,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kRows = 128, kTile = 64, kThreads = 256;
 constexpr float kSlack = 8.0f;
-// Scales of V that the products take: the weights times them, and their reciprocals,
-// stay far from the ends of the exponent's range (a weight of 2^-46 times the least
-// one is still a normal number).
-constexpr float kScaleMin = 0x1p-80f, kScaleMax = 0x1p80f;
+// int8: weights are held 2^kShift times as large, so that the scales of V that the
+// products take reach from 2^-110 to 2^50 (values of an ordinary model lie between 2^-30
+// and 2^20): a weight of 2^-46 times the least scale is still a normal number, and
+// 2^8 times the largest one and its reciprocal are far from the other end.
+constexpr float kShift = 30.0f, kScaleMin = 0x1p-110f, kScaleMax = 0x1p50f;
 
 __device__ __forceinline__ v16f mfma32(uint4 a, uint4 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
@@ -120,12 +121,14 @@ struct RowOut {
 // row does not see takes no part at all and a value is code * scale whatever the
 // scale: for workgroups whose edge tiles hold infinities or NaN in V (the products
 // of a tile would carry them to every row as 0 * inf), or whose tiles hold scales of
-// V outside kScaleMin to kScaleMax.  The whole workgroup, `buf` 516 floats of LDS;
-// tile_token(i) is the first token of tile i, i from i0 to i1 - 1.
+// V outside kScaleMin to kScaleMax.  About 12 us a row and tile, for what should
+// not be there at all.  The whole workgroup, `buf` 512 floats of LDS; tile_token(i) is
+// the first token of tile i, i from i0 to i1 - 1.
 template <bool INT8, bool FP32, class F>
 __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t token, int h, int kvh,
                           int pos, F tile_token, int i0, int i1, RowOut out, float *buf) {
     float *q = buf, *p = buf + 256;
+    int64_t *vecs = reinterpret_cast<int64_t *>(p + 128);  // of the tile's tokens, -1: not seen
     const int tid = threadIdx.x, D = a.c.D;
     const int low = a.window ? pos - a.window + 1 : 0;
     __syncthreads();
@@ -139,6 +142,19 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
             return (float)(int8_t)pool[vec * D + d] * scales[vec];
         else
             return bf16_lo(reinterpret_cast<const uint16_t *>(pool)[vec * D + d]);
+    };
+    auto key8 = [&](int64_t vec, int d, float (&k)[8]) {
+        if constexpr (INT8) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(a.c.k + vec * D + d);
+            const float s = a.c.ks[vec];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) k[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (j % 4 * 8)) * s;
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4 *>(a.c.k + (vec * D + d) * 2);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[2 * j] = bf16_lo(v[j]), k[2 * j + 1] = bf16_hi(v[j]);
+        }
     };
     auto vector = [&](int t) {
         const int pg = kv_page(a.c, table, t);
@@ -154,11 +170,18 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
             float s = -INFINITY;
             if (vec >= 0) {
                 float x = 0.0f;
-                for (int d = 0; d < D; ++d) x = __builtin_fmaf(q[d], value(a.c.k, a.c.ks, vec, d), x);
+#pragma unroll 1
+                for (int d = 0; d < D; d += 8) {
+                    float k[8];
+                    key8(vec, d, k);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x = __builtin_fmaf(q[d + j], k[j], x);
+                }
                 s = x * a.scale * 1.44269504088896340736f;
             }
             const float mn = fmaxf(m, wave_max(s));
-            p[tid] = vec >= 0 ? __builtin_amdgcn_exp2f(s - mn) : -1.0f;  // (-1: not seen)
+            vecs[tid] = vec;
+            p[tid] = vec >= 0 ? __builtin_amdgcn_exp2f(s - mn) : 0.0f;
             if (tid == 0) p[kTile] = mn;
         }
         __syncthreads();
@@ -167,11 +190,14 @@ __device__ void plain_row(const KvAttnArgs &a, const int32_t *table, int64_t tok
         m = mn;
         l *= alpha;
         o *= alpha;
+#pragma unroll 4
         for (int j = 0; j < kTile; ++j) {
-            if (p[j] < 0.0f) continue;
+            const int64_t vj = vecs[j];
             l += p[j];
-            const int64_t vj = vector(t0 + j);
-            if (tid < D) o = __builtin_fmaf(p[j], value(a.c.v, a.c.vs, vj, tid), o);
+            if (tid < D) {
+                const float v = value(a.c.v, a.c.vs, max(vj, (int64_t)0), tid);
+                o = __builtin_fmaf(p[j], vj >= 0 ? v : 0.0f, o);
+            }
         }
     }
     if (out.parts > 1) {
@@ -342,12 +368,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                 const int at = wave * 16 + lane, t = tile_token(i) + at;
                 sks[buf][at] = ks;
                 const bool fits = fabsf(vs) >= kScaleMin && fabsf(vs) <= kScaleMax;
-                // (not finite or far off: what a row sees, plain_row takes as it is; an
-                // unseen token's weight of zero stays zero)
-                if (!fits && vs != 0.0f && t <= pos1 && (t >= low0 || t < a.sinks) &&
-                    !(gone_of(i) >> wave & 1))
+                const bool finite = fabsf(vs) < INFINITY;
+                // (far off, or not finite for some rows only: plain_row takes what a row
+                // sees as it is.  An unseen token's weight of zero stays zero; what is not
+                // finite for all rows reaches all of them)
+                if (!fits && vs != 0.0f && (edge || finite) && t <= pos1 &&
+                    (t >= low0 || t < a.sinks) && !(gone_of(i) >> wave & 1))
                     odd = 1;
-                const float v = fits || (FP32 && vs == 0.0f) ? vs : 1.0f;
+                const float v = fits || (FP32 && vs == 0.0f) || !(edge || finite) ? vs : 1.0f;
                 svs[buf][at] = v;
                 if constexpr (!FP32) {
                     const float inv = 1.0f / v;
@@ -480,7 +508,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
         }
-        const float mu = m == -INFINITY ? 0.0f : -m;
+        const float mu = m == -INFINITY ? 0.0f : INT8 ? kShift - m : -m;
         constexpr int kAheadV = 1;
         constexpr int kVMask = 0x2 | 0x4 | 0x400;  // VALU, SALU and transcendentals may pass
         uint4 vf[kAheadV + 1];
@@ -559,8 +587,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
             const int64_t rr = row0 + i;
             const int tk = (int)(rr / G), h = kvh * G + (int)(rr - (int64_t)tk * G);
             plain_row<INT8, FP32>(a, table, c0 + tk, h, kvh, len - (int)nq + tk, tile_token, i0, i1,
-                            RowOut{(c0 + tk) * a.hq + h, part, parts},
-                            reinterpret_cast<float *>(lds));
+                            RowOut{(c0 + tk) * a.hq + h, part, parts}, reinterpret_cast<float *>(lds));
         }
         return;
     }
@@ -578,7 +605,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && !FP32 ? 2 : 1) void k_kv_pre
                     *reinterpret_cast<float4 *>(to + at) = float4{
                         o[d][4 * r4], o[d][4 * r4 + 1], o[d][4 * r4 + 2], o[d][4 * r4 + 3]};
             }
-        if (half == 0) to[D] = m, to[D + 1] = l;
+        if (half == 0) to[D] = INT8 ? m - kShift : m, to[D + 1] = l;
         return;
     }
 
