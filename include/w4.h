@@ -448,6 +448,11 @@ size_t kv_attention_workspace_bytes(int64_t rows, int64_t B, int64_t q_heads, in
  *   workspace  kv_attention_workspace_bytes(B, B, q_heads, heads, head_dim)
  *           bytes, 256-byte aligned; scratch.
  * Results do not depend on the order in which workgroups run.
+ * K, V and scales of tokens that a row does not see take no part in it, whatever
+ * they hold.  A NaN in a row's query or in K of a token that it sees makes the
+ * whole row NaN, one in V its own dimension (one in V's scale the whole row).
+ * An infinity there makes the outputs that it reaches infinite or NaN, NaN also
+ * where the formula has an infinity, or a weight of 0.
  * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN,
  * W4_ERR_WORKSPACE or W4_ERR_HIP. */
 int kv_decode_attention(const kv_cache *cache, int64_t layer, const void *q, int x_dtype,
@@ -477,13 +482,13 @@ int kv_copy_pages(const kv_cache *dst, const int32_t *dst_ids, const kv_cache *s
                   const int32_t *src_ids, int64_t n, void *stream);
 
 /* Give every slot the pages for add[s] more tokens.  A slot needs the pages of
- * its row from the first -1 at or after entry lens[s] / page_size up to entry
+ * its row from the first entry below 0 at or after lens[s] / page_size up to entry
  * ceil((lens[s] + add[s]) / page_size) - 1.  Free pages (refs 0) are dealt in
  * ascending order, to slots in ascending order, each page's refs set to 1; slot
  * s is served (ok[s] = 1) if it needs none or the needs of slots 0 .. s
  * together are not more than the free pages, else left as it was (ok[s] = 0).
- * add[s] <= 0 needs nothing; a slot whose row is too short, or with a length outside
- * [0, W * page_size], needs nothing and has ok 0.
+ * add[s] <= 0 needs nothing and has ok 1; else a slot whose row is too short, or with
+ * a length outside [0, W * page_size], needs nothing and has ok 0.
  *   workspace  8 * S + 256 bytes, 16-byte aligned. */
 int kv_reserve(int32_t *table, int64_t S, int64_t W, const int32_t *lens, int32_t *refs,
                int64_t pages, int64_t page_size, const int32_t *add, int32_t *ok,
@@ -495,9 +500,9 @@ int kv_reserve(int32_t *table, int64_t S, int64_t W, const int32_t *lens, int32_
  * pages are dealt in ascending order to the forks that need one in order; fork
  * i is granted (ok[i] = 1) if the needs of forks 0 .. i together are not more
  * than the free pages.  Not granted: a slot outside [0, S), a child that is
- * not empty (length 0 and first entry -1) or that an earlier i names too, a
- * parent whose length is outside [0, W * page_size] or whose last partial page
- * is none.  A child that is not granted stays empty.  Pages that a parent has
+ * not empty (length 0 and first entry -1), a parent whose length is outside
+ * [0, W * page_size] or whose last partial page is none, and a child that an
+ * earlier fork with none of these faults names too.  A child that is not granted stays empty.  Pages that a parent has
  * reserved beyond its length stay its own.
  *   workspace  16 * n + 256 bytes, 16-byte aligned. */
 int kv_fork(const kv_cache *cache, int32_t *table, int64_t S, int64_t W, int32_t *lens,

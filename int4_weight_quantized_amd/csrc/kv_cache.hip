@@ -11,8 +11,9 @@ namespace w4 {
 // A group of LPV lanes (8, 16 or 32: head_dim up to 64, 128, 256) handles one
 // head's vector of one token, 8 values a lane; blockIdx.y selects K or V.
 // Bound by memory: each value is read once and written once (179 MB of prompts, 8
-// heads of 128, bf16: 41 to 43 us, 4.2 to 4.4 TB/s; a large copy: 4.9).  The row's values are loaded
-// before the search for its sequence, and stored past the caches.
+// heads of 128, bf16: 42 us, 4.2 TB/s; a large copy: 4.9; 224 MB of fp32 to int8: 60
+// us).  The row's values are loaded before the search for its sequence, and stored past
+// the caches.
 
 struct KvPlace {
     int64_t token;   // row of the call, or -1
@@ -215,7 +216,7 @@ hipError_t launch_kv_gather(const KvView &c, bool int8, const KvRows &r, void *k
 // and their scales), i below n or, on the device, below *count.  A workgroup
 // copies up to kCopyChunk bytes of one plane's page per step of a grid-stride
 // loop, four 16-byte loads a thread in flight, past the caches; bound by memory
-// (each byte read once and written once: 3.2 GB in 623 us, 5.2 TB/s, where a large
+// (each byte read once and written once: 3.2 GB in 614 to 629 us, 5.2 TB/s, where a large
 // library copy reaches 4.9; a compaction in a loop: 508 us, with 2048 workgroups
 // 528, with 65536 500, where 256 forks take 82 us with either of the latter two).
 constexpr int64_t kCopyChunk = 32768, kCopyBlocks = 8192;
@@ -296,8 +297,9 @@ hipError_t launch_kv_copy_pages(const KvPlanes &dst, const int32_t *dst_ids, con
 // Reference counts and tables are small next to the pages; one workgroup walks
 // them, so that ranks come from prefix sums in index order and every result is
 // the same whatever the timing.  Bound by the latency of one step after another (a
-// fork's plan 5.9 us at 300 pages and 7.8 at 6000, a compaction's 4.2 at 257 and 6.8
-// at 1536).
+// fork's plan 5.5 us at 300 pages and 8.0 at 6000, a compaction's 4.0 at 257 and 6.8
+// at 1536, a reservation 4.5 for 64 slots of 8000 pages where none is due and 5.6
+// where every slot gets one).
 constexpr int kPlan = 1024;
 
 // Inclusive prefix sum over the workgroup; `total` gets the sum of all.

@@ -29,11 +29,12 @@
 // leave columns free (4 rows of 3 terms, 8 rows of 2), the terms take columns
 // of their own: one MFMA for all of them, and the columns are summed at the end.
 //
-// Bound by memory.  4 sequences of 131072 tokens, 64 / 8 heads of 128, bf16: 331
+// Bound by memory.  4 sequences of 131072 tokens, 64 / 8 heads of 128, bf16: 330
 // us, 6.5 TB/s (a plain read: 7.05; this kernel's loads without its products: 325
-// us).  64 ragged sequences up to 8191, 32 / 8 heads, int8, fp32 activations: 100
-// us, 5.3 TB/s.  One token behind 700 with a window of 512, 4 / 1 heads of 256: 10.7
-// us, launch and memory latency.
+// us).  64 ragged sequences up to 8191, 32 / 8 heads, int8, fp32 activations: 99
+// us, 5.3 TB/s (a tile of int8 has half the bytes of one of bf16 in flight, and the
+// same work).  One token behind 700 with a window of 512, 4 / 1 heads of 256: 10.5
+// us, one workgroup's three rounds of tiles one after another.
 #include "kv_attn.h"
 
 namespace w4 {
@@ -174,7 +175,9 @@ __device__ __forceinline__ int pair_units(const Span &s) {
 }
 
 // Query heads in groups of up to 16 that share a cache head: `per_head` groups
-// for each of the cache's heads, `rows` rows at most in one.
+// for each of the cache's heads, `rows` rows at most in one.  Each group reads K and
+// V for itself (4 sequences of 131072 tokens, 8 cache heads of 128, bf16: 330 us for
+// 64 query heads, 339 for 128, 656 for 256).
 struct KvHeads {
     int group, rows, per_head, count;
     __host__ __device__ explicit KvHeads(const KvAttnArgs &a) {
@@ -620,6 +623,16 @@ __global__ __launch_bounds__(256) void k_kv_decode_join(KvAttnArgs a) {
 
 namespace {
 
+// Up to so many tokens (of a table's row, or visible in the window) a pair is one
+// workgroup's; longer ones are split and joined by a second launch.  us, whole / split,
+// equally long sequences, 4 query heads a cache head of 128, bf16:
+//   pairs    512 tokens    1024          2048           4096
+//      1      6.5 /  9.4    8.9 /  9.8    13.5 /  10.1   22.3 /  11.0
+//     64      6.9 / 11.9   11.0 / 14.5    23.4 /  21.0   43.3 /  29.4
+//    256     11.6 / 17.5   22.1 / 28.9    42.4 /  48.0   81.9 /  87.8
+//   1024     47.8 / 50.3   85.6 / 93.0   160.9 / 172.7  318.4 / 334.0
+// The host knows the table's width, not the lengths: where a row is half full, the
+// column to its left decides.
 constexpr int64_t kWholeTokens = 2048;
 
 template <int DP, bool INT8>

@@ -33,12 +33,13 @@
 // terms: 318 us where one took 265, int8); fp32 ones are three bf16 terms, q and
 // weights alike, so that products keep 24 bits.  Sums and statistics are fp32.
 //
-// 8192 causal tokens, 32 / 8 heads of 128, bf16: 537 us, 1.02 PFLOP/s (large
-// library products in bf16: 1.21 to 1.36).  The MFMAs are busy 49% of 1.07 million
-// cycles.  A schedule with the next tile's scores beside this one's exponentials was
-// no faster (557 us where 559 without) and spilled registers for int8.
-// int8 adds the conversion of codes and the scales: 277 us for ragged prompts up to
-// 8000 with a window of 1024, 16 / 4 heads of 128.  256 rows a workgroup share that
+// 8192 causal tokens, 32 / 8 heads of 128, bf16: 527 to 557 us by card, 0.99 to 1.04
+// PFLOP/s (large library products in bf16: 1.21 to 1.36).  The MFMAs are busy 49% of
+// 1.08 million cycles.  A schedule with the next tile's scores beside this one's
+// exponentials was no faster (557 us where 559 without) and spilled registers for int8.
+// fp32 activations, three products for one: 1472 us.
+// int8 adds the conversion of codes and the scales: 277 to 289 us for ragged prompts up
+// to 8000 with a window of 1024, 16 / 4 heads of 128.  256 rows a workgroup share that
 // work among more rows, but took 274 us where 128 took 265 (both before the weights'
 // sum was taken from their rounded values).
 #include "kv_attn.h"
@@ -694,7 +695,15 @@ int64_t row_tiles(int64_t T, int64_t B, int64_t G) { return T * G / kRows + B; }
 // Few workgroups leave the chip idle and run through their tokens one tile after
 // another: their tiles are then split over up to kMaxParts parts, as many as two
 // workgroups a CU take, and joined by a second launch (3 chunks of up to 37 tokens
-// behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 13 us split).
+// behind up to 1001, fp32, 12 / 4 heads of 64: 36 us in one part, 13.5 us split).
+// us of one chunk, 4 query heads a cache head of 128, bf16, in one part / up to 256 /
+// 512 / 1024 workgroups:
+//   rows, cache heads   behind 64                   1024                        16384 tokens
+//      1, 2              8.7 / 10.0 / 10.0 / 10.0   26.5 / 11.5 / 11.5 / 11.5   309 / 29 / 29 / 29
+//    128, 8             12.0 / 17.0 / 17.2 / 17.0   29.8 / 22.8 / 27.1 / 29.8   314 / 67 / 55 / 55
+//    512, 8             19.8 / 19.4 / 37.1 / 41.4   37.2 / 37.1 / 42.8 / 48.3   322 / 322 / 172 / 171
+// 512 is for the long contexts, where it saves most; many rows behind few tokens pay
+// for it, since the host does not know the lengths.
 constexpr int64_t kPartBlocks = 512;
 int64_t most_parts(int64_t T, int64_t B, int64_t hq, int64_t heads) {
     const int64_t groups = row_tiles(T, B, hq / heads) * heads;
