@@ -349,7 +349,8 @@ __global__ __launch_bounds__(
         v4f o[VD] = {};
         float m = -INFINITY, l = 0.0f;
         // int8: weights are 2^shift times as large where the wave's first scales of V
-        // are tiny, so that the terms of their products stay normal numbers
+        // that are not zero are tiny, so that the terms of their products stay normal
+        // numbers
         float shift = 0.0f;
         bool fresh = true;
         const int32_t *table = a.c.table + b * a.c.W;
@@ -463,8 +464,10 @@ __global__ __launch_bounds__(
                     for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(t.vs[h][r]));
                 big = fmaxf(big, __shfl_xor(big, 16, kWave));
                 big = fmaxf(big, __shfl_xor(big, 32, kWave));
-                shift = __builtin_amdgcn_readfirstlane(big < 0x1p-60f) ? 40.0f : 0.0f;
-                fresh = false;
+                if (__builtin_amdgcn_readfirstlane(big > 0.0f)) {
+                    fresh = false;
+                    if (__builtin_amdgcn_readfirstlane(big < 0x1p-60f)) shift = 40.0f, l *= 0x1p40f;
+                }
             }
             float mt = x[0][0];
 #pragma unroll

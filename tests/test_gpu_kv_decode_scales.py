@@ -50,3 +50,27 @@ def test_one_far_part(w4, W, q):
     y = w4.kv_decode_attention(x, cache, 0, table, tl)
     ok, worst = close(y, *attend(x, K[0], V[0], [699], 0, 0, D ** -0.5))
     assert ok, worst
+
+
+@pytest.mark.parametrize("q", ["bf16", "fp32"])
+@pytest.mark.parametrize("W", [0, 400])
+@pytest.mark.parametrize("power", [-105, -40, 89])
+def test_zeros_before_far_scales(w4, power, W, q):
+    """Scales of zero, and pages that are gone, in front of the far ones say nothing
+    about them."""
+    hq, heads, D, pairs = 8, 2, 128, [(700, 1)]
+    cache, table, tl, K, V, x, cu = setup(w4, heads, D, pairs, hq, q, 122)
+    cache.v_scale.mul_(2.0 ** power)
+    hole = torch.zeros(700, dtype=torch.bool)
+    for lo in range(0, 512, 128):
+        pages = table[0, lo // 16:lo // 16 + 2].long()
+        cache.v_scale[0, pages] = 0.0
+        V[0][lo:lo + 32] = 0.0
+        table[0, lo // 16 + 2:lo // 16 + 4] = -1
+        hole[lo + 32:lo + 64] = True
+    if W:
+        table = torch.nn.functional.pad(table, (0, W - table.shape[1]), value=-1).contiguous()
+    y = w4.kv_decode_attention(x, cache, 0, table, tl)
+    y = (y.float() * 2.0 ** -power).to(y.dtype)
+    ok, worst = close(y, *attend(x, K[0], V[0], [699], 0, 0, D ** -0.5, hole))
+    assert ok, worst
