@@ -524,6 +524,141 @@ int kv_compact(const kv_cache *cache, const int32_t *table, int64_t S, int64_t W
                const int32_t *refs, int32_t *table_out, int32_t *refs_out, int32_t *live,
                void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- What a decoder layer runs around its quantized projections: the norm in
+ * front of one, rotary positions behind one, adapters beside one. */
+
+/* Element type of rms_norm's output. */
+typedef enum { RMS_BF16 = 0, RMS_FP32 = 1 } rms_dtype;
+
+/* Root-mean-square norm of rows, with the residual's addition in front:
+ *   h   = fl(x + residual) (fp32; x itself without a residual),
+ *   r   = fl(1 / sqrt(mean_k(h^2) + eps)), the mean and the root in fp64,
+ *   out = fl(fl(h * r) * fl(offset + weight)), rounded once more for bf16.
+ *   x        M rows of K values of x_dtype (kv_x_dtype), x_stride elements apart
+ *            (at least K);
+ *   residual [M][K] of x_dtype, or NULL;
+ *   weight   [K] fp32, or NULL for ones (fl(offset + 1)); offset 0, or 1 where
+ *            weights are stored as their distance from one;
+ *   sum      [M][K] of x_dtype: h, rounded for bf16 (the norm takes it as it was
+ *            before); required with a residual, NULL without.  It may be the
+ *            residual itself, or x itself where x_stride is K;
+ *   out      [M][K] of out_dtype; it overlaps nothing else.
+ * eps is finite and not below 0.  1 <= K <= W4_MAX_K, 1 <= M <= 2^23.
+ * Since h^2 is exact in fp64 and the mean is rounded far below fp32, the result
+ * does not depend on the order of the sum: every kernel gives the same bits.
+ * A row with a value that is not finite gives what the formula gives for it
+ * (NaN, or 0 beside an infinity); other rows are not touched by it.  A row of
+ * zeros with eps 0 is NaN.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
+int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
+             const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+             void *out, int out_dtype, void *stream);
+
+/* The same with int8 rows as w4a8_linear_q takes them: Xq [M][K] and sx [M] are
+ * bit for bit those that a8_quantize_act makes of rms_norm's fp32 output.  A row
+ * whose output has a value that is not finite gets the scale NaN (its codes are
+ * then unspecified), so that a product of it is NaN.
+ * (For awq_quantize_act of the output, pass fl(offset + weight) / s and offset 0:
+ * the division by powers of two is exact.) */
+int a8_rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
+                const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+                int8_t *Xq, float *sx, void *stream);
+
+/* Rotary positions.  The first rot_dim values of a head are rot_dim / 2 pairs;
+ * pair i of a token at position p is turned by p * turns[i] full turns:
+ *   (a, b) -> (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))),
+ *   c, s = fp32 of magnitude * cos, sin(2 pi p turns[i]), computed in fp64;
+ * the other values stay as they are.  rot_dim is even, from 2 to 512. */
+typedef enum {
+    ROPE_HALF = 0, /* pair i: values i and i + rot_dim / 2 */
+    ROPE_PAIRS = 1 /* pair i: values 2 i and 2 i + 1       */
+} rope_layout;
+
+typedef struct {
+    const double *turns; /* device, [rot_dim / 2] */
+    int64_t rot_dim;
+    int layout;       /* rope_layout */
+    double magnitude; /* finite      */
+} rope_spec;
+
+/* How frequencies are stretched for contexts beyond the trained one. */
+typedef enum {
+    ROPE_PLAIN = 0,
+    ROPE_LINEAR = 1, /* every position divided by factor                        */
+    ROPE_NTK = 2,    /* base grows by factor^(rot_dim / (rot_dim - 2))          */
+    ROPE_YARN = 3,   /* by the pair's index between the pairs that make `fast`
+                        and `slow` turns within context tokens: the faster ones
+                        stay, the slower ones are divided by factor, a ramp
+                        between; magnitude 0.1 ln(factor) + 1                   */
+    ROPE_BANDS = 4   /* the same by the pair's own turns within context tokens,
+                        a ramp from slow to fast, magnitude 1                   */
+} rope_scaling;
+
+/* turns[i] = base^(-2 i / rot_dim) / (2 pi), stretched, into HOST memory
+ * [rot_dim / 2], and the magnitude (1 unless said above).  base > 1, factor >= 1
+ * (not used by ROPE_PLAIN); context >= 1 and fast > slow > 0 for ROPE_YARN and
+ * ROPE_BANDS (not used by the others).  Host code only.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE or W4_ERR_ARG. */
+int rope_frequencies(int64_t rot_dim, double base, int scaling, double factor, int64_t context,
+                     double fast, double slow, double *turns, double *magnitude);
+
+/* Rotate x: T rows of [heads][head_dim] values of x_dtype, x_stride elements
+ * apart (at least heads * head_dim), row t at position pos[t] (int32, any value).
+ *   out  rows of the same values, out_stride apart; it may be x itself with the
+ *        same stride, and overlaps it in no other way.  bf16: rounded once.
+ * head_dim is a multiple of 8 up to 512, not below rot_dim; 1 <= T <= 2^23,
+ * T * heads <= 2^26.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
+int rope_rotate(const rope_spec *rope, const void *x, int x_dtype, int64_t x_stride, int64_t T,
+                int64_t heads, int64_t head_dim, const int32_t *pos, void *out,
+                int64_t out_stride, void *stream);
+
+/* kv_append with rotary positions, and the queries rotated beside it: row
+ * cu[b] + t of q, k and v is the token at position start[b] + t.
+ *   q        T rows of [q_heads][head_dim], q_stride elements apart; rotated
+ *            into q_out (rows out_stride apart; q itself with the same stride,
+ *            or no overlap), also where the token has no page.  Rows of no
+ *            sequence and of skipped ones (start[b] < 0) keep what q_out held.
+ *   k        rotated in fp32, then rounded or quantized into the cache;
+ *   v        as in kv_append; everything else too.
+ * T * (q_heads + 2 * heads) <= 2^26; head_dim not below rot_dim.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
+int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, const void *q,
+                   const void *k, const void *v, int x_dtype, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, int64_t q_heads, int64_t T, int64_t B, const int32_t *table,
+                   int64_t W, const int32_t *start, const int32_t *cu, void *q_out,
+                   int64_t out_stride, void *stream);
+
+/* Low-rank adapters of many requests at once, beside a product whose weights
+ * they share: with a = ids[m],
+ *   Y[m][n] += scales[a] * sum_j (sum_k X[m][k] * A[a][j][k]) * B[a][n][j].
+ *   X       M rows of K values of x_dtype (kv_x_dtype), x_stride elements apart;
+ *   ids     [M] int32; a row whose id is outside [0, adapters) stays as it is;
+ *   A       [adapters][rank][K], B [adapters][N][rank] bf16 bit patterns;
+ *   scales  [adapters] fp32, or NULL for ones;
+ *   ranks   [adapters] int32, or NULL: adapter a uses its first ranks[a] of rank
+ *           rows of A and columns of B (limited to [0, rank]); what the others
+ *           hold takes no part, NaN included;
+ *   Y       M rows of N fp32, y_stride elements apart (the product's output, or
+ *           a slice of its columns); it overlaps no other argument.
+ * Products of X, A and B keep fp32 accuracy for both types of X, sums are fp32;
+ * a row's result does not depend on the other rows, nor on their order.  Rows
+ * of one adapter that lie next to each other are computed together.
+ *   workspace  lora_workspace_bytes(M, K, N, rank) bytes, 256-byte aligned; scratch.
+ * 1 <= rank <= 256, 1 <= adapters <= 2^20, 1 <= M <= 2^23, 1 <= K <= W4_MAX_K,
+ * 1 <= N < 2^31, adapters * rank * max(K, N) <= 2^46.
+ * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN,
+ * W4_ERR_WORKSPACE or W4_ERR_HIP. */
+int lora_add(const void *X, int x_dtype, int64_t x_stride, int64_t M, int64_t K, int64_t N,
+             const int32_t *ids, const uint16_t *A, const uint16_t *B, int64_t adapters,
+             int64_t rank, const float *scales, const int32_t *ranks, float *Y, int64_t y_stride,
+             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of lora_add's device workspace; 0 for invalid sizes.  It does not fall
+ * when M, K, N or rank grow: the workspace of a program's largest call serves
+ * its smaller ones. */
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank);
+
 /* Static description of a status code (never NULL). */
 const char *w4_status_string(int status);
 

@@ -31,7 +31,10 @@ functions carry the C names:
 * ``KVCache``, ``kv_append``, ``kv_gather``, ``kv_decode_attention``,
   ``kv_prefill_attention``, ``kv_reserve``, ``kv_fork``, ``kv_free``,
   ``kv_copy_pages``, ``kv_compact`` -- the paged key-value cache between the
-  quantized projections of a decoder layer (``kv.py``).
+  quantized projections of a decoder layer (``kv.py``);
+* ``rms_norm``, ``a8_rms_norm``, ``Rope``, ``rope_frequencies``, ``rope_rotate``,
+  ``kv_append_rope``, ``lora_add`` -- norms in front of those projections, rotary
+  positions behind them, adapters beside them (``layer.py``).
 
 There is no CPU fallback: without the built library (``build.py``) or
 without a GPU every call raises.
@@ -124,6 +127,7 @@ def lib():
             "w4_time_next_kernel": ([_P, _P], ctypes.c_int),
         }
         sigs.update(SIGNATURES)
+        sigs.update(LAYER_SIGNATURES)
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -727,3 +731,6 @@ from .kv import (KV_BF16, KV_INT8, KV_X_BF16, KV_X_FP32, SIGNATURES, KVCache,  #
                  kv_append, kv_attention_workspace_bytes, kv_compact, kv_copy_pages,
                  kv_decode_attention, kv_fork, kv_free, kv_gather, kv_prefill_attention,
                  kv_reserve)
+from .layer import (LAYER_SIGNATURES, RMS_BF16, RMS_FP32, ROPE_HALF, ROPE_PAIRS, Rope,  # noqa: E402
+                    a8_rms_norm, kv_append_rope, lora_add, lora_workspace_bytes, rms_norm,
+                    rope_frequencies, rope_rotate)

@@ -23,7 +23,7 @@ ARCH = "gfx950"
 
 SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "w4a16.hip", "generic.hip", "probe.hip", "kv_cache.hip",
            "kv_attn.hip", "kv_decode.hip", "kv_prefill.hip",
-           "kv_api.cpp", "api.cpp"]
+           "kv_api.cpp", "norm.hip", "rope.hip", "lora.hip", "layer_api.cpp", "api.cpp"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

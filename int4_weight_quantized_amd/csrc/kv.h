@@ -31,6 +31,13 @@ struct KvView {
     int pages, heads, D, shift;  // page_size = 1 << shift
 };
 
+// One layer of a checked cache with the call's table, and the checks of a call that
+// writes or reads rows of tokens (strides in elements, align in bytes); kv_api.cpp.
+KvView kv_layer_view(const kv_cache *c, int64_t layer, const int32_t *table, int64_t W);
+int check_kv_rows(const kv_cache *c, int64_t layer, const void *k, const void *v, int x_dtype,
+                  int64_t ldk, int64_t ldv, int64_t T, int64_t B, const int32_t *table, int64_t W,
+                  const int32_t *start, const int32_t *cu, size_t align);
+
 // Places of a call's tokens: rows cu[b] .. cu[b + 1] - 1 (cu NULL: row b) are
 // sequence b's tokens from position start[b].
 struct KvRows {

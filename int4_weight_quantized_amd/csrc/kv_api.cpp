@@ -63,23 +63,6 @@ int check_workspace(const void *ws, size_t bytes, size_t need, size_t align) {
     return aligned(ws, align) ? W4_OK : W4_ERR_ALIGN;
 }
 
-w4::KvView layer_view(const kv_cache *c, int64_t layer, const int32_t *table, int64_t W) {
-    const int64_t vecs = c->pages * c->heads * c->page_size;
-    const int64_t bytes = vecs * c->head_dim * (c->dtype == KV_BF16 ? 2 : 1);
-    w4::KvView v{};
-    v.k = static_cast<uint8_t *>(c->k) + layer * bytes;
-    v.v = static_cast<uint8_t *>(c->v) + layer * bytes;
-    v.ks = c->k_scale ? c->k_scale + layer * vecs : nullptr;
-    v.vs = c->v_scale ? c->v_scale + layer * vecs : nullptr;
-    v.table = table;
-    v.W = W;
-    v.pages = (int)c->pages;
-    v.heads = (int)c->heads;
-    v.D = (int)c->head_dim;
-    v.shift = log2_page(c->page_size);
-    return v;
-}
-
 w4::KvPlanes planes(const kv_cache *c) {
     const int64_t vecs = c->heads * c->page_size;
     w4::KvPlanes p{};
@@ -95,25 +78,6 @@ w4::KvPlanes planes(const kv_cache *c) {
 }
 
 hipStream_t hip_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
-
-// Checks shared by kv_append and kv_gather (strides in elements).
-int check_rows(const kv_cache *c, int64_t layer, const void *k, const void *v, int x_dtype,
-               int64_t ldk, int64_t ldv, int64_t T, int64_t B, const int32_t *table, int64_t W,
-               const int32_t *start, const int32_t *cu, size_t align) {
-    int rc = check_cache(c);
-    if (rc != W4_OK) return rc;
-    if (!k || !v || !start) return W4_ERR_NULL;
-    if ((rc = check_table(table, B, W)) != W4_OK) return rc;
-    if (x_dtype != KV_X_BF16 && x_dtype != KV_X_FP32) return W4_ERR_ARG;
-    if (layer < 0 || layer >= c->layers) return W4_ERR_ARG;
-    const int64_t row = c->heads * c->head_dim;
-    if (T < 1 || T > kMaxVectors / c->heads || (!cu && T != B)) return W4_ERR_SHAPE;
-    if (ldk < row || ldv < row || ldk > kMaxValues / T || ldv > kMaxValues / T)
-        return W4_ERR_SHAPE;
-    if (!aligned(k, align) || !aligned(v, align) || !aligned(start, 4) || !aligned(cu, 4))
-        return W4_ERR_ALIGN;
-    return W4_OK;
-}
 
 int attention(const kv_cache *c, int64_t layer, const void *q, int x_dtype,
               int64_t ldq, int64_t T, int64_t B, int64_t hq, const int32_t *table, int64_t W,
@@ -138,7 +102,7 @@ int attention(const kv_cache *c, int64_t layer, const void *q, int x_dtype,
                          kv_attention_workspace_bytes(T, B, hq, c->heads, c->head_dim), 256);
     if (rc != W4_OK) return rc;
     w4::KvAttnArgs a{};
-    a.c = layer_view(c, layer, table, W);
+    a.c = w4::kv_layer_view(c, layer, table, W);
     a.int8 = c->dtype == KV_INT8;
     a.fp32 = x_dtype == KV_X_FP32;
     a.q = q;
@@ -160,17 +124,53 @@ int attention(const kv_cache *c, int64_t layer, const void *q, int x_dtype,
 
 }  // namespace
 
+w4::KvView w4::kv_layer_view(const kv_cache *c, int64_t layer, const int32_t *table, int64_t W) {
+    const int64_t vecs = c->pages * c->heads * c->page_size;
+    const int64_t bytes = vecs * c->head_dim * (c->dtype == KV_BF16 ? 2 : 1);
+    w4::KvView v{};
+    v.k = static_cast<uint8_t *>(c->k) + layer * bytes;
+    v.v = static_cast<uint8_t *>(c->v) + layer * bytes;
+    v.ks = c->k_scale ? c->k_scale + layer * vecs : nullptr;
+    v.vs = c->v_scale ? c->v_scale + layer * vecs : nullptr;
+    v.table = table;
+    v.W = W;
+    v.pages = (int)c->pages;
+    v.heads = (int)c->heads;
+    v.D = (int)c->head_dim;
+    v.shift = log2_page(c->page_size);
+    return v;
+}
+
+// Checks shared by kv_append, kv_gather and kv_append_rope (strides in elements).
+int w4::check_kv_rows(const kv_cache *c, int64_t layer, const void *k, const void *v, int x_dtype,
+               int64_t ldk, int64_t ldv, int64_t T, int64_t B, const int32_t *table, int64_t W,
+               const int32_t *start, const int32_t *cu, size_t align) {
+    int rc = check_cache(c);
+    if (rc != W4_OK) return rc;
+    if (!k || !v || !start) return W4_ERR_NULL;
+    if ((rc = check_table(table, B, W)) != W4_OK) return rc;
+    if (x_dtype != KV_X_BF16 && x_dtype != KV_X_FP32) return W4_ERR_ARG;
+    if (layer < 0 || layer >= c->layers) return W4_ERR_ARG;
+    const int64_t row = c->heads * c->head_dim;
+    if (T < 1 || T > kMaxVectors / c->heads || (!cu && T != B)) return W4_ERR_SHAPE;
+    if (ldk < row || ldv < row || ldk > kMaxValues / T || ldv > kMaxValues / T)
+        return W4_ERR_SHAPE;
+    if (!aligned(k, align) || !aligned(v, align) || !aligned(start, 4) || !aligned(cu, 4))
+        return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
 extern "C" {
 
 int kv_append(const kv_cache *cache, int64_t layer, const void *k, const void *v, int x_dtype,
               int64_t k_stride, int64_t v_stride, int64_t T, int64_t B, const int32_t *table,
               int64_t W, const int32_t *start, const int32_t *cu, void *stream) {
-    const int rc = check_rows(cache, layer, k, v, x_dtype, k_stride, v_stride, T, B, table, W,
+    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, k_stride, v_stride, T, B, table, W,
                               start, cu, x_dtype == KV_X_FP32 ? 4 : 2);
     if (rc != W4_OK) return rc;
     const w4::KvRows rows{start, cu, T, B};
     return w4::finish_call(
-        "kv_append", w4::launch_kv_append(layer_view(cache, layer, table, W),
+        "kv_append", w4::launch_kv_append(w4::kv_layer_view(cache, layer, table, W),
                                           cache->dtype == KV_INT8, rows, k, v,
                                           x_dtype == KV_X_FP32, k_stride, v_stride,
                                           hip_stream(stream)));
@@ -180,12 +180,12 @@ int kv_gather(const kv_cache *cache, int64_t layer, void *k, void *v, int x_dtyp
               int64_t B, const int32_t *table, int64_t W, const int32_t *start,
               const int32_t *cu, void *stream) {
     const int64_t row = cache ? cache->heads * cache->head_dim : 0;
-    const int rc = check_rows(cache, layer, k, v, x_dtype, row, row, T, B, table, W, start, cu,
+    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, row, row, T, B, table, W, start, cu,
                               16);
     if (rc != W4_OK) return rc;
     const w4::KvRows rows{start, cu, T, B};
     return w4::finish_call(
-        "kv_gather", w4::launch_kv_gather(layer_view(cache, layer, table, W),
+        "kv_gather", w4::launch_kv_gather(w4::kv_layer_view(cache, layer, table, W),
                                           cache->dtype == KV_INT8, rows, k, v,
                                           x_dtype == KV_X_FP32, hip_stream(stream)));
 }

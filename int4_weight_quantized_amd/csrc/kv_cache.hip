@@ -51,37 +51,6 @@ __device__ __forceinline__ KvPlace kv_place(const KvView &c, const KvRows &r) {
     return p;
 }
 
-template <bool FP32>
-__device__ __forceinline__ void load8(const void *x, int64_t at, bool vec, float (&f)[8]) {
-    if constexpr (FP32) {
-        const float *s = reinterpret_cast<const float *>(x) + at;
-        if (vec) {
-            const float4 a = *reinterpret_cast<const float4 *>(s);
-            const float4 b = *reinterpret_cast<const float4 *>(s + 4);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = s[j];
-        }
-    } else {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(x) + at;
-        if (vec) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(s);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float((uint32_t)s[j] << 16);
-        }
-    }
-}
-
-// Rounding to the cache's type happens once, here: bf16 half to even, or int8 with
-// the scale absmax * fl(1 / 127) of the head's vector (one multiplication, within
-// one unit in the last place of the quotient) and codes rne(fl(x / scale)).  A
-// vector with a value that is not finite has no int8 form: its scale is NaN.
 template <bool INT8, bool FP32, int LPV>
 __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const void *k,
                                                    const void *v, int64_t ldk, int64_t ldv,
@@ -96,29 +65,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
                     f);
     }
     const KvPlace p = kv_place<LPV>(c, r);
-    const bool on = p.vec >= 0 && d < c.D;
-    uint8_t *pool = isv ? c.v : c.k;
-    if constexpr (INT8) {
-        // the bits of |x| order as the values do, infinity and NaN above them all
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
-        if (!on) return;
-        const float s = m < 0x7F800000u ? __uint_as_float(m) * (1.0f / 127.0f) : NAN;
-        uint32_t w[2] = {};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j / 4] |= (uint32_t)(quant_code(f[j], s, -128.0f, 127.0f) & 0xFF) << (j % 4 * 8);
-        *reinterpret_cast<uint2 *>(pool + p.vec * c.D + d) = uint2{w[0], w[1]};
-        if (d == 0) (isv ? c.vs : c.ks)[p.vec] = s;
-    } else {
-        if (!on) return;
-        const u32x4 o = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7])};
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(pool + (p.vec * c.D + d) * 2));
-    }
+    kv_store8<INT8, LPV>(c, isv, p.vec, d, p.vec >= 0 && d < c.D, f);
 }
 
 template <bool INT8, bool FP32, int LPV>
