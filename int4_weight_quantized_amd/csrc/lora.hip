@@ -1,14 +1,35 @@
 // Low-rank adapters beside a shared product:
 //   Y[m] += scale_a ((X[m] A_a^T) B_a^T), a = ids[m].
-// Two launches: S = X A^T into the workspace, then Y += scale S B^T.
+// Two launches: S = X A^T into the workspace, in parts of K, then Y += scale S B^T.
+//
+// Rows are taken in tiles of 16 or 32 as they lie.  A workgroup goes through the
+// different adapters that its tile names (a ballot over the tile's ids; slots of
+// workgroups share them out) and computes the tile's rows of one adapter at a
+// time, so that no plan, no sorting and no atomics are needed and a row's result
+// does not depend on its neighbours.
+//
+// Products are bf16 MFMAs (16 x 16 x 32) with fp32 sums.  An fp32 value of X, and
+// every value of S, is three bf16 terms of 8 bits each, cut off one after the
+// other: they hold its 24 bits exactly (down to 2^-110, below which the last terms
+// would be subnormal), and the largest values do not round up to infinity.
+#include <algorithm>
+#include <type_traits>
+
 #include "kv_common.h"
 #include "layer.h"
 
 namespace w4 {
 
+struct LoraPlan {
+    int slots, splits, kc;  // workgroups of a tile, parts of K, length of a part
+    int rp;                 // rank, rounded up to 16: a row of S
+    int nc;                 // channels of a workgroup of the second launch
+};
+
+// ------------------------------------------------------------------ helpers
 // The adapter of a row, or -1.
 __device__ __forceinline__ int lora_id(const LoraArgs &a, int64_t m) {
-    const int id = a.ids[m];
+    const int id = m < a.M ? a.ids[m] : -1;
     return (uint32_t)id < (uint32_t)a.adapters ? id : -1;
 }
 
@@ -16,60 +37,375 @@ __device__ __forceinline__ int lora_rank(const LoraArgs &a, int id) {
     return a.ranks ? min(max(a.ranks[id], 0), a.rank) : a.rank;
 }
 
-__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+// f(adapter, mask of its rows) for every slots-th different adapter of the tile
+// whose ids the lanes hold.
+template <typename F>
+__device__ __forceinline__ void each_adapter(int id, int slot, int slots, F f) {
+    uint64_t todo = __ballot(id >= 0);
+    for (int i = 0; todo; ++i) {
+        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t match = __ballot(id == cur);
+        todo &= ~match;
+        if (i % slots == slot) f(cur, match);
+    }
+}
 
-__device__ __forceinline__ float wave_add(float v) {
+// Eight floats as three bf16 terms, each the upper half of what is left.
+__device__ __forceinline__ void cut3(const float (&f)[8], v8bf (&out)[3]) {
+    uint32_t r[8];
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
-}
-
-// Any sizes and alignment.  One wave a row of X and row j = blockIdx.y of A.
-template <bool FP32>
-__global__ __launch_bounds__(256) void k_lora_down_any(LoraArgs a) {
-    const int64_t m = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-    const int j = blockIdx.y;
-    if (m >= a.M) return;
-    const int id = lora_id(a, m);
-    if (id < 0 || j >= lora_rank(a, id)) return;
-    const uint16_t *row = a.A + ((int64_t)id * a.rank + j) * a.K;
-    float acc = 0.0f;
-    for (int64_t k = threadIdx.x % kWave; k < a.K; k += kWave) {
-        float x;
-        if constexpr (FP32) x = reinterpret_cast<const float *>(a.X)[m * a.ldx + k];
-        else x = bf16_value(reinterpret_cast<const uint16_t *>(a.X)[m * a.ldx + k]);
-        acc = __builtin_fmaf(x, bf16_value(row[k]), acc);
-    }
-    acc = wave_add(acc);
-    if (threadIdx.x % kWave == 0) a.ws[m * a.rank + j] = acc;
-}
-
-// One thread an output; rows beyond the grid's in strides of it.
-__global__ __launch_bounds__(256) void k_lora_up_any(LoraArgs a) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
-    for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
-        const int id = lora_id(a, m);
-        if (id < 0) continue;
-        const int rank = lora_rank(a, id);
-        const uint16_t *col = a.B + ((int64_t)id * a.N + n) * a.rank;
-        float acc = 0.0f;
-        for (int j = 0; j < rank; ++j)
-            acc = __builtin_fmaf(a.ws[m * a.rank + j], bf16_value(col[j]), acc);
-        float *y = a.Y + m * a.ldy + n;
-        *y += (a.scales ? a.scales[id] : 1.0f) * acc;
+    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(f[j]);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(r[2 * j + 1], r[2 * j], 0x07060302u);
+        out[t] = __builtin_bit_cast(v8bf, uint4{w[0], w[1], w[2], w[3]});
+        if (t < 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) - __uint_as_float(r[j] & 0xFFFF0000u));
+        }
     }
 }
 
-size_t lora_ws_bytes(int64_t M, int64_t, int64_t, int64_t rank) { return (size_t)M * rank * 4; }
+// Eight bf16 from p, the first `n` of them valid, zeros for the others.
+__device__ __forceinline__ uint4 some8(const uint16_t *p, int n) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0u;
+    return uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+}
+
+// Which of eight bf16 to keep, the first `n` (the others may hold anything).
+__device__ __forceinline__ uint4 keep8(int n) {
+    auto two = [&](int i) { return n > i + 1 ? ~0u : n > i ? 0xFFFFu : 0u; };
+    return uint4{two(0), two(2), two(4), two(6)};
+}
+
+__device__ __forceinline__ uint4 and8(uint4 w, uint4 k) {
+    return uint4{w.x & k.x, w.y & k.y, w.z & k.z, w.w & k.w};
+}
+
+// Eight values of X as operand terms.
+template <bool FP32> struct Chunk;
+template <> struct Chunk<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void some(const float *p, int n) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = j < n ? p[j] : 0.0f;
+        a = float4{f[0], f[1], f[2], f[3]}, b = float4{f[4], f[5], f[6], f[7]};
+    }
+    __device__ __forceinline__ void terms(v8bf (&out)[3]) const {
+        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        cut3(f, out);
+    }
+};
+template <> struct Chunk<false> {
+    uint4 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void some(const uint16_t *p, int n) { w = some8(p, n); }
+    __device__ __forceinline__ void terms(v8bf (&out)[1]) const { out[0] = __builtin_bit_cast(v8bf, w); }
+};
+
+__device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ X A^T
+// Workgroup (tile and slot, part of K, 16 RC rows of A): its four waves take a
+// quarter of the part each and add their sums in LDS.  A is the first operand
+// and X the second, so that a lane ends with four neighbouring values of a row
+// of S.  X is read once (for every 16 RC ranks), straight into registers.
+template <bool FP32, bool VEC, int MT, int RC>
+__global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
+    constexpr int U = FP32 ? 4 / MT : MT * RC >= 8 ? 1 : 8 / (MT * RC);  // k-steps in flight
+    constexpr int kTerms = FP32 ? 3 : 1;
+    using X = std::conditional_t<FP32, float, uint16_t>;
+    __shared__ v4f red[4][MT * RC][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int c16 = lane % 16, q8 = lane / 16 * 8;
+    const int64_t m0 = (int64_t)(blockIdx.x / p.slots) * (16 * MT);
+    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+    const int K = (int)a.K, r0 = blockIdx.z * (16 * RC);
+    const int kw = p.kc / 4, k0 = blockIdx.y * p.kc + wave * kw, k1 = min(k0 + kw, K);
+    const X *row = reinterpret_cast<const X *>(a.X) + (m0 + c16) * a.ldx + q8;
+    each_adapter(id, blockIdx.x % p.slots, p.slots, [&](int cur, uint64_t match) {
+        const int rank = lora_rank(a, cur);
+        if (r0 >= rank) return;
+        const int ranks = min(rank - r0, 16 * RC);
+        const uint16_t *A = a.A + ((int64_t)cur * a.rank + r0) * a.K;
+        const auto ra = make_rsrc(A, (int64_t)ranks * a.K * 2);  // (beyond it: zeros)
+        v4f acc[MT][RC];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int k = k0; k < k1; k += 32 * U) {
+            Chunk<FP32> x[U][MT] = {};
+            uint4 w[U][RC];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < RC; ++c) {
+                    const int kk = k + 32 * u + q8, j = 16 * c + c16;
+                    if constexpr (VEC) w[u][c] = bload16(ra, (j * K + kk) * 2);
+                    else w[u][c] = some8(A + (int64_t)j * K + kk, j < ranks ? k1 - kk : 0);
+                }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if (!(match >> (16 * t + c16) & 1)) continue;
+                const X *src = row + 16 * t * a.ldx + k;
+                if (VEC && k + 32 * U <= k1) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) x[u][t].load(src + 32 * u);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int left = k1 - (k + 32 * u + q8);
+                        if constexpr (VEC) {
+                            if (left > 0) x[u][t].load(src + 32 * u);
+                        } else {
+                            x[u][t].some(src + 32 * u, left);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    v8bf f[kTerms];
+                    x[u][t].terms(f);
+#pragma unroll
+                    for (int c = 0; c < RC; ++c)
+#pragma unroll
+                        for (int i = kTerms - 1; i >= 0; --i)
+                            acc[t][c] = mfma(__builtin_bit_cast(v8bf, w[u][c]), f[i], acc[t][c]);
+                }
+        }
+        lds_barrier();  // (the sums of the adapter before have been read)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
+        lds_barrier();
+        for (int i = threadIdx.x; i < MT * RC * kWave; i += 256) {
+            const int tc = i / kWave, m = 16 * (tc / RC) + i % 16;
+            const int j = r0 + 16 * (tc % RC) + i % kWave / 16 * 4;
+            if (!(match >> m & 1) || j >= p.rp) continue;
+            v4f s = red[0][tc][i % kWave];
+#pragma unroll
+            for (int v = 1; v < 4; ++v) s += red[v][tc][i % kWave];
+            *reinterpret_cast<v4f *>(a.ws + ((int64_t)blockIdx.y * a.M + m0 + m) * p.rp + j) = s;
+        }
+    });
+}
+
+// ------------------------------------------------------------------ Y += S B^T
+// Workgroup (tile and slot, nc channels).  The parts of S are added in order into
+// LDS once; a wave keeps the terms of its rows in registers while it goes through
+// 16 channels of B at a time.  B is the first operand, so that a lane has four
+// neighbouring channels of a row of Y.
+template <bool VEC, bool YVEC, int MT, int KS>
+__global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
+    constexpr int NU = 4;  // blocks of 16 channels whose loads are in flight
+    constexpr int kRow = 32 * KS + 4;
+    __shared__ __align__(16) float S[16 * MT][kRow];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int c16 = lane % 16, q = lane / 16;
+    const int64_t m0 = (int64_t)(blockIdx.x / p.slots) * (16 * MT);
+    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+    const int64_t n0 = (int64_t)blockIdx.y * p.nc;
+    const int len = (int)min((int64_t)p.nc, a.N - n0);
+    float *row = a.Y + (m0 + c16) * a.ldy + n0 + 4 * q;
+    each_adapter(id, blockIdx.x % p.slots, p.slots, [&](int cur, uint64_t match) {
+        const int rank = lora_rank(a, cur);
+        if (rank == 0) return;
+        const uint16_t *B = a.B + ((int64_t)cur * a.N + n0) * a.rank;
+        const auto rb = make_rsrc(B, (int64_t)len * a.rank * 2);  // (beyond it: zeros)
+        int at[KS];      // this lane's bytes of a block of 16 channels
+        uint4 keep[KS];  // and which of its values count
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int j = 32 * s + 8 * q;
+            at[s] = j < rank ? (c16 * a.rank + j) * 2 : kOOB;
+            keep[s] = keep8(rank - j);
+        }
+        uint4 w[NU][KS];
+        v4f y[NU][MT];
+        auto load_b = [&](int n) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int ch = n + 16 * u;
+                    if constexpr (VEC) w[u][s] = bload16(rb, at[s] + ch * a.rank * 2);
+                    else w[u][s] = some8(B + (int64_t)(ch + c16) * a.rank + 32 * s + 8 * q,
+                                         ch + c16 < len ? rank - 32 * s - 8 * q : 0);
+                }
+        };
+        // Y's four channels of a lane, read (STORE false) or written
+        auto each_y = [&](int n, auto f) {
+            const bool full = YVEC && n + 16 * NU <= len;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if (!(match >> (16 * t + c16) & 1)) continue;
+                float *dst = row + 16 * t * a.ldy + n;
+                if (full) {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) f(dst + 16 * u, y[u][t], 4);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) f(dst + 16 * u, y[u][t], len - (n + 16 * u + 4 * q));
+                }
+            }
+        };
+        auto read = [](const float *src, v4f &v, int left) {
+            if constexpr (YVEC) {
+                if (left > 0) v = *reinterpret_cast<const v4f *>(src);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) v[e] = src[e];
+            }
+        };
+        auto write = [](float *dst, const v4f &v, int left) {
+            if constexpr (YVEC) {
+                if (left > 0) *reinterpret_cast<v4f *>(dst) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) dst[e] = v[e];
+            }
+        };
+        int n = wave * (16 * NU);
+        load_b(n);  // (in flight while S is summed)
+        each_y(n, read);
+        const float scale = a.scales ? a.scales[cur] : 1.0f;
+        lds_barrier();  // (the rows of the adapter before have been read)
+        const int64_t part = a.M * p.rp;
+        for (int i = threadIdx.x; i < 16 * MT * 8 * KS; i += 256) {
+            const int m = i / (8 * KS), j = i % (8 * KS) * 4;
+            v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+            if ((match >> m & 1) && j < rank) {
+                const float *src = a.ws + (m0 + m) * p.rp + j;
+#pragma unroll 4
+                for (int k = 0; k < p.splits; ++k, src += part)
+                    s += *reinterpret_cast<const v4f *>(src);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = j + e < rank ? s[e] : 0.0f;
+            }
+            *reinterpret_cast<v4f *>(&S[m][j]) = s;
+        }
+        lds_barrier();
+        v8bf f[MT][KS][3];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                float v[8];
+                const float *src = &S[16 * t + c16][32 * s + 8 * q];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = src[e];
+                cut3(v, f[t][s]);
+            }
+        for (;;) {
+            const int next = n + 64 * NU;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+#pragma unroll
+                        for (int i = 2; i >= 0; --i)
+                            acc = mfma(__builtin_bit_cast(v8bf, VEC ? and8(w[u][s], keep[s]) : w[u][s]),
+                                       f[t][s][i], acc);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[u][t][e] = __builtin_fmaf(scale, acc[e], y[u][t][e]);
+                }
+            if (next < len) load_b(next);
+            each_y(n, write);
+            if (next >= len) break;
+            n = next;
+            each_y(n, read);
+        }
+    });
+}
+
+// ------------------------------------------------------------------ launches
+constexpr int kMaxSplits = 16;
+constexpr int64_t kSplitRows = 32768;  // rows of S in the workspace beyond the first part, at most
+
+static int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// S in up to 1 + min(15, 32768 / M) parts: the size grows with M and rank alone.
+size_t lora_ws_bytes(int64_t M, int64_t, int64_t, int64_t rank) {
+    const int64_t rows = M + std::min(M * (kMaxSplits - 1), kSplitRows);
+    return (size_t)rows * (size_t)round16(rank) * 4;
+}
+
+template <bool FP32, bool VEC, int MT>
+static void go_down(const LoraArgs &a, const LoraPlan &p, int64_t tiles, hipStream_t st) {
+    const int rc = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+    const dim3 g((unsigned)(tiles * p.slots), (unsigned)p.splits,
+                 (unsigned)((a.rank + 16 * rc - 1) / (16 * rc)));
+    if (rc == 1) launch_kv(k_lora_down<FP32, VEC, MT, 1>, g, dim3(256), 0, st, a, p);
+    else if (rc == 2) launch_kv(k_lora_down<FP32, VEC, MT, 2>, g, dim3(256), 0, st, a, p);
+    else launch_kv(k_lora_down<FP32, VEC, MT, 4>, g, dim3(256), 0, st, a, p);
+}
+
+template <bool VEC, bool YVEC, int MT>
+static void go_up(const LoraArgs &a, const LoraPlan &p, int64_t tiles, hipStream_t st) {
+    const dim3 g((unsigned)(tiles * p.slots), (unsigned)((a.N + p.nc - 1) / p.nc));
+    if (a.rank <= 32) launch_kv(k_lora_up<VEC, YVEC, MT, 1>, g, dim3(256), 0, st, a, p);
+    else if (a.rank <= 64) launch_kv(k_lora_up<VEC, YVEC, MT, 2>, g, dim3(256), 0, st, a, p);
+    else if (a.rank <= 128) launch_kv(k_lora_up<VEC, YVEC, MT, 4>, g, dim3(256), 0, st, a, p);
+    else if constexpr (MT == 1) launch_kv(k_lora_up<VEC, YVEC, 1, 8>, g, dim3(256), 0, st, a, p);
+}
+
+template <int MT>
+static void go(const LoraArgs &a, hipStream_t st) {
+    auto at16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    const int64_t tiles = (a.M + 16 * MT - 1) / (16 * MT);
+    // workgroups of a tile: as many as its adapters can use, or 2048 of the call
+    auto slots = [&](int64_t others) {
+        const int64_t most = std::min<int64_t>(16 * MT, a.adapters);
+        return (int)std::max<int64_t>(1, std::min<int64_t>(most, 2048 / std::max<int64_t>(1, others)));
+    };
+    LoraPlan p{};
+    p.rp = (int)round16(a.rank);
+    int64_t splits = std::min<int64_t>(1 + std::min<int64_t>(kMaxSplits - 1, kSplitRows / a.M),
+                                       std::min<int64_t>((a.K + 511) / 512, (1024 + tiles - 1) / tiles));
+    p.kc = (int)(((a.K + splits - 1) / splits + 127) / 128 * 128);
+    p.splits = (int)((a.K + p.kc - 1) / p.kc);
+    p.slots = slots(tiles * p.splits);
+    const bool xv = a.K % 8 == 0 && at16(a.X) && at16(a.A) && a.ldx * (a.fp32 ? 4 : 2) % 16 == 0;
+    if (a.fp32) xv ? go_down<true, true, MT>(a, p, tiles, st) : go_down<true, false, MT>(a, p, tiles, st);
+    else xv ? go_down<false, true, MT>(a, p, tiles, st) : go_down<false, false, MT>(a, p, tiles, st);
+
+    const bool bv = a.rank % 8 == 0 && at16(a.B);
+    const bool yv = a.N % 4 == 0 && a.ldy % 4 == 0 && at16(a.Y);
+    const int64_t chunks = (a.N + 255) / 256;
+    const int64_t per = std::max<int64_t>(
+        std::max<int64_t>(1, std::min<int64_t>(4, tiles * chunks / 2048)), (chunks + 65534) / 65535);
+    p.nc = (int)(256 * per);
+    p.slots = slots(tiles * ((a.N + p.nc - 1) / p.nc));
+    if (bv) yv ? go_up<true, true, MT>(a, p, tiles, st) : go_up<true, false, MT>(a, p, tiles, st);
+    else yv ? go_up<false, true, MT>(a, p, tiles, st) : go_up<false, false, MT>(a, p, tiles, st);
+}
 
 hipError_t launch_lora(const LoraArgs &a, const char **path, hipStream_t st) {
-    *path = "lora_any";
-    const dim3 down((unsigned)((a.M + 3) / 4), (unsigned)a.rank);
-    const dim3 up((unsigned)((a.N + 255) / 256), (unsigned)(a.M < 65535 ? a.M : 65535));
-    if (a.fp32) launch_kv(k_lora_down_any<true>, down, dim3(256), 0, st, a);
-    else launch_kv(k_lora_down_any<false>, down, dim3(256), 0, st, a);
-    launch_kv(k_lora_up_any, up, dim3(256), 0, st, a);
+    *path = "lora";
+    if (a.M <= 256 || a.rank > 128) go<1>(a, st);
+    else go<2>(a, st);
     return hipGetLastError();
 }
 
