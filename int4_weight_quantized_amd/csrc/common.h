@@ -38,6 +38,11 @@ __device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, int off) {
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
+// A 16-byte store; outside the range nothing is written.
+__device__ __forceinline__ void bstore16(__amdgpu_buffer_rsrc_t r, int off, uint4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 0);
+}
+
 // Streaming 16-byte load (non-temporal hint): for data a kernel reads exactly
 // once, the packed weights of the decode GEMVs, so that the stream does not
 // displace cache lines that are reused.

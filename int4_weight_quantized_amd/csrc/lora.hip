@@ -23,10 +23,16 @@ namespace w4 {
 struct LoraPlan {
     int slots, splits, kc;  // workgroups of a tile, parts of K, length of a part
     int rp;                 // rank, rounded up to 16: a row of S
+    int tiles;
     int nc;                 // channels of a workgroup of the second launch
 };
 
 // ------------------------------------------------------------------ helpers
+// (uniform: the loops of a wave then run on scalars)
+__device__ __forceinline__ int wave_id() {
+    return __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+}
+
 // The adapter of a row, or -1.
 __device__ __forceinline__ int lora_id(const LoraArgs &a, int64_t m) {
     const int id = m < a.M ? a.ids[m] : -1;
@@ -91,10 +97,6 @@ __device__ __forceinline__ uint4 and8(uint4 w, uint4 k) {
 template <bool FP32> struct Chunk;
 template <> struct Chunk<true> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
-    }
     __device__ __forceinline__ void some(const float *p, int n) {
         float f[8];
 #pragma unroll
@@ -108,7 +110,6 @@ template <> struct Chunk<true> {
 };
 template <> struct Chunk<false> {
     uint4 w;
-    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void some(const uint16_t *p, int n) { w = some8(p, n); }
     __device__ __forceinline__ void terms(v8bf (&out)[1]) const { out[0] = __builtin_bit_cast(v8bf, w); }
 };
@@ -118,64 +119,70 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 }
 
 // ------------------------------------------------------------------ X A^T
+// The four waves' sums into this part's rows of S.
+template <int MT, int RC>
+__device__ __forceinline__ void write_sums(const LoraArgs &a, const LoraPlan &p,
+                                           const v4f (*red)[MT * RC][kWave], int64_t m0, int r0,
+                                           uint64_t match) {
+    for (int i = threadIdx.x; i < MT * RC * kWave; i += 256) {
+        const int tc = i / kWave, m = 16 * (tc / RC) + i % 16;
+        const int j = r0 + 16 * (tc % RC) + i % kWave / 16 * 4;
+        if (!(match >> m & 1) || j >= p.rp) continue;
+        v4f s = red[0][tc][i % kWave];
+#pragma unroll
+        for (int v = 1; v < 4; ++v) s += red[v][tc][i % kWave];
+        *reinterpret_cast<v4f *>(a.ws + ((int64_t)blockIdx.x * a.M + m0 + m) * p.rp + j) = s;
+    }
+}
+
 // Workgroup (tile and slot, part of K, 16 RC rows of A): its four waves take a
 // quarter of the part each and add their sums in LDS.  A is the first operand
 // and X the second, so that a lane ends with four neighbouring values of a row
 // of S.  X is read once (for every 16 RC ranks), straight into registers.
-template <bool FP32, bool VEC, int MT, int RC>
+template <bool FP32, int MT, int RC>
 __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
     constexpr int U = FP32 ? 4 / MT : MT * RC >= 8 ? 1 : 8 / (MT * RC);  // k-steps in flight
     constexpr int kTerms = FP32 ? 3 : 1;
     using X = std::conditional_t<FP32, float, uint16_t>;
     __shared__ v4f red[4][MT * RC][kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave, wave = wave_id();
     const int c16 = lane % 16, q8 = lane / 16 * 8;
-    const int64_t m0 = (int64_t)(blockIdx.x / p.slots) * (16 * MT);
-    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
     const int K = (int)a.K, r0 = blockIdx.z * (16 * RC);
-    const int kw = p.kc / 4, k0 = blockIdx.y * p.kc + wave * kw, k1 = min(k0 + kw, K);
-    const X *row = reinterpret_cast<const X *>(a.X) + (m0 + c16) * a.ldx + q8;
-    each_adapter(id, blockIdx.x % p.slots, p.slots, [&](int cur, uint64_t match) {
+    const int kw = p.kc / 4, k0 = blockIdx.x * p.kc + wave * kw, k1 = min(k0 + kw, K);
+    for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
+    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+    const X *rows = reinterpret_cast<const X *>(a.X) + m0 * a.ldx;
+    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
         const int rank = lora_rank(a, cur);
         if (r0 >= rank) return;
         const int ranks = min(rank - r0, 16 * RC);
         const uint16_t *A = a.A + ((int64_t)cur * a.rank + r0) * a.K;
-        const auto ra = make_rsrc(A, (int64_t)ranks * a.K * 2);  // (beyond it: zeros)
         v4f acc[MT][RC];
+        bool on[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t) {
+            on[t] = match >> (16 * t + c16) & 1;
 #pragma unroll
             for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
         for (int k = k0; k < k1; k += 32 * U) {
-            Chunk<FP32> x[U][MT] = {};
+            Chunk<FP32> x[U][MT];
             uint4 w[U][RC];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int c = 0; c < RC; ++c) {
                     const int kk = k + 32 * u + q8, j = 16 * c + c16;
-                    if constexpr (VEC) w[u][c] = bload16(ra, (j * K + kk) * 2);
-                    else w[u][c] = some8(A + (int64_t)j * K + kk, j < ranks ? k1 - kk : 0);
+                    w[u][c] = some8(A + (int64_t)j * K + kk, j < ranks ? k1 - kk : 0);
                 }
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if (!(match >> (16 * t + c16) & 1)) continue;
-                const X *src = row + 16 * t * a.ldx + k;
-                if (VEC && k + 32 * U <= k1) {
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) x[u][t].load(src + 32 * u);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int left = k1 - (k + 32 * u + q8);
-                        if constexpr (VEC) {
-                            if (left > 0) x[u][t].load(src + 32 * u);
-                        } else {
-                            x[u][t].some(src + 32 * u, left);
-                        }
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const int kk = k + 32 * u + q8;
+                    x[u][t].some(rows + (16 * t + c16) * a.ldx + kk, on[t] ? k1 - kk : 0);
                 }
-            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -195,36 +202,145 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
 #pragma unroll
             for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
         lds_barrier();
-        for (int i = threadIdx.x; i < MT * RC * kWave; i += 256) {
-            const int tc = i / kWave, m = 16 * (tc / RC) + i % 16;
-            const int j = r0 + 16 * (tc % RC) + i % kWave / 16 * 4;
-            if (!(match >> m & 1) || j >= p.rp) continue;
-            v4f s = red[0][tc][i % kWave];
-#pragma unroll
-            for (int v = 1; v < 4; ++v) s += red[v][tc][i % kWave];
-            *reinterpret_cast<v4f *>(a.ws + ((int64_t)blockIdx.y * a.M + m0 + m) * p.rp + j) = s;
-        }
+        write_sums<MT, RC>(a, p, red, m0, r0, match);
     });
+    }
+}
+
+// The same for aligned operands: stages of 128 k go through LDS by direct loads,
+// whole row pieces of 256 and 512 bytes side by side, since the operands' own layout
+// (neighbouring lanes, different rows) costs the address unit four times the cycles
+// (8192 rows, K 4096: 45 us straight into registers, 134 MB).  16-byte pieces of a row are
+// stored at their index xor the row, so that 16 rows' reads of one piece hit all
+// banks.  Wave w takes k-step w of each stage; three stages, two of them in flight.
+template <bool FP32, int MT, int RC>
+__global__ __launch_bounds__(256) void k_lora_down_lds(LoraArgs a, LoraPlan p) {
+    constexpr int kTerms = FP32 ? 3 : 1;
+    constexpr int kStage = 128, kSlots = 3;
+    constexpr int kXRow = kStage * (FP32 ? 4 : 2), kARow = kStage * 2;  // bytes
+    constexpr int kXBytes = 16 * MT * kXRow, kBytes = kXBytes + 16 * RC * kARow;
+    constexpr int kXLoads = kXBytes / 4096, kALoads = RC;  // 1 KB loads of a wave and stage
+    constexpr int kLoads = kXLoads + kALoads;
+    __shared__ __align__(1024) uint8_t lds[kSlots * kBytes];
+    static_assert(4 * MT * RC * 1024 <= kSlots * kBytes, "the sums fit the stages' memory");
+    const int lane = threadIdx.x % kWave, wave = wave_id();
+    const int c16 = lane % 16, q = lane / 16;
+    const int K = (int)a.K, r0 = blockIdx.z * (16 * RC);
+    const int k0 = blockIdx.x * p.kc, k1 = min(k0 + p.kc, K);
+    const uint32_t base = lds_addr(lds);
+    for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
+    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+    const v4i rx = buffer_desc(reinterpret_cast<const uint8_t *>(a.X) + m0 * a.ldx * (FP32 ? 4 : 2),
+                               kMaxRange);
+    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
+        const int rank = lora_rank(a, cur);
+        if (r0 >= rank) return;
+        const int ranks = min(rank - r0, 16 * RC);
+        const v4i ra = buffer_desc(a.A + ((int64_t)cur * a.rank + r0) * a.K,
+                                   (int64_t)ranks * a.K * 2);
+        // this lane's piece of each of the wave's loads: byte offset at k = 0, and its k
+        constexpr int kXPieces = kXRow / 16, kAPieces = kARow / 16;
+        int xoff[kXLoads], xk[kXLoads], aoff[kALoads], ak[kALoads];
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const int n = (wave * kXLoads + i) * kWave + lane, m = n / kXPieces;
+            xk[i] = ((n % kXPieces) ^ (m % 16)) * (FP32 ? 4 : 8);
+            xoff[i] = match >> m & 1 ? (int)(m * a.ldx + xk[i]) * (FP32 ? 4 : 2) : kOOB;
+        }
+#pragma unroll
+        for (int i = 0; i < kALoads; ++i) {
+            const int n = (wave * kALoads + i) * kWave + lane, j = n / kAPieces;
+            ak[i] = ((n % kAPieces) ^ (j % 16)) * 8;
+            aoff[i] = j < ranks ? (j * K + ak[i]) * 2 : kOOB;
+        }
+        auto fetch = [&](int k, int slot) {
+            const uint32_t to = base + slot * kBytes;
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i)
+                dma16(rx, to + (wave * kXLoads + i) * 1024,
+                      k + xk[i] < k1 && xoff[i] != kOOB ? xoff[i] + k * (FP32 ? 4 : 2) : kOOB, 0);
+#pragma unroll
+            for (int i = 0; i < kALoads; ++i)
+                dma16(ra, to + kXBytes + (wave * kALoads + i) * 1024,
+                      k + ak[i] < k1 && aoff[i] != kOOB ? aoff[i] + k * 2 : kOOB, 0);
+        };
+        v4f acc[MT][RC];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+        wait_and_barrier<0>();  // (LDS is free, and no store is counted among the loads)
+        fetch(k0, 0);
+        if (k0 + kStage < k1) fetch(k0 + kStage, 1);
+        int slot = 0;
+        for (int k = k0; k < k1; k += kStage) {
+            if (k + kStage < k1) wait_and_barrier<kLoads>();
+            else wait_and_barrier<0>();
+            if (k + 2 * kStage < k1) fetch(k + 2 * kStage, slot == 0 ? 2 : slot - 1);
+            const uint8_t *from = lds + slot * kBytes;
+            const int kk = k + 32 * wave + 8 * q;
+            uint4 w[RC];
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {
+                w[c] = *reinterpret_cast<const uint4 *>(from + kXBytes + (16 * c + c16) * kARow +
+                                                        ((4 * wave + q) ^ c16) * 16);
+                if (kk >= k1) w[c] = uint4{};
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const uint8_t *row = from + (16 * t + c16) * kXRow;
+                Chunk<FP32> x;
+                if constexpr (FP32) {
+                    x.a = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q) ^ c16) * 16);
+                    x.b = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q + 1) ^ c16) * 16);
+                } else {
+                    x.w = *reinterpret_cast<const uint4 *>(row + ((4 * wave + q) ^ c16) * 16);
+                }
+                if (kk >= k1) x = Chunk<FP32>{};
+                v8bf f[kTerms];
+                x.terms(f);
+#pragma unroll
+                for (int c = 0; c < RC; ++c)
+#pragma unroll
+                    for (int i = kTerms - 1; i >= 0; --i)
+                        acc[t][c] = mfma(__builtin_bit_cast(v8bf, w[c]), f[i], acc[t][c]);
+            }
+            slot = slot == kSlots - 1 ? 0 : slot + 1;
+        }
+        v4f(*red)[MT * RC][kWave] = reinterpret_cast<v4f(*)[MT * RC][kWave]>(lds);
+        lds_barrier();  // (every wave has read its last stage)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
+        lds_barrier();
+        write_sums<MT, RC>(a, p, red, m0, r0, match);
+    });
+    }
 }
 
 // ------------------------------------------------------------------ Y += S B^T
 // Workgroup (tile and slot, nc channels).  The parts of S are added in order into
 // LDS once; a wave keeps the terms of its rows in registers while it goes through
-// 16 channels of B at a time.  B is the first operand, so that a lane has four
-// neighbouring channels of a row of Y.
+// 64 channels of B at a time (B is the first operand: a lane has four neighbouring
+// channels of a row).  The 256 channels of the four waves change lanes in LDS, so
+// that Y is read and written in whole pieces of 1 KB of a row, and only its own rows.
 template <bool VEC, bool YVEC, int MT, int KS>
 __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
     constexpr int NU = 4;  // blocks of 16 channels whose loads are in flight
     constexpr int kRow = 32 * KS + 4;
     __shared__ __align__(16) float S[16 * MT][kRow];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    __shared__ __align__(16) float D[16 * MT][260];
+    const int lane = threadIdx.x % kWave, wave = wave_id();
     const int c16 = lane % 16, q = lane / 16;
-    const int64_t m0 = (int64_t)(blockIdx.x / p.slots) * (16 * MT);
-    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
-    const int64_t n0 = (int64_t)blockIdx.y * p.nc;
+    const int64_t n0 = (int64_t)blockIdx.x * p.nc;
     const int len = (int)min((int64_t)p.nc, a.N - n0);
-    float *row = a.Y + (m0 + c16) * a.ldy + n0 + 4 * q;
-    each_adapter(id, blockIdx.x % p.slots, p.slots, [&](int cur, uint64_t match) {
+    for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
+    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+    float *rows = a.Y + m0 * a.ldy + n0;
+    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
         const int rank = lora_rank(a, cur);
         if (rank == 0) return;
         const uint16_t *B = a.B + ((int64_t)cur * a.N + n0) * a.rank;
@@ -238,53 +354,45 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
             keep[s] = keep8(rank - j);
         }
         uint4 w[NU][KS];
-        v4f y[NU][MT];
+        v4f y[4 * MT];  // of rows wave, wave + 4, ...: this lane's four channels of 256
         auto load_b = [&](int n) {
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    const int ch = n + 16 * u;
-                    if constexpr (VEC) w[u][s] = bload16(rb, at[s] + ch * a.rank * 2);
+                    const int ch = n + 64 * wave + 16 * u;
+                    if constexpr (VEC) w[u][s] = bload16(rb, (int)((uint32_t)at[s] + (uint32_t)(ch * a.rank * 2)));
                     else w[u][s] = some8(B + (int64_t)(ch + c16) * a.rank + 32 * s + 8 * q,
                                          ch + c16 < len ? rank - 32 * s - 8 * q : 0);
                 }
         };
-        // Y's four channels of a lane, read (STORE false) or written
         auto each_y = [&](int n, auto f) {
-            const bool full = YVEC && n + 16 * NU <= len;
+            const int left = len - (n + 4 * lane);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if (!(match >> (16 * t + c16) & 1)) continue;
-                float *dst = row + 16 * t * a.ldy + n;
-                if (full) {
-#pragma unroll
-                    for (int u = 0; u < NU; ++u) f(dst + 16 * u, y[u][t], 4);
+            for (int i = 0; i < 4 * MT; ++i) {
+                const int m = wave + 4 * i;
+                if (!(match >> m & 1)) continue;
+                float *at = rows + m * a.ldy + n + 4 * lane;
+                if constexpr (YVEC) {
+                    if (left > 0) f(i, m, [&](v4f &v) { v = *reinterpret_cast<const v4f *>(at); },
+                                    [&](const v4f &v) { *reinterpret_cast<v4f *>(at) = v; });
                 } else {
+                    f(i, m,
+                      [&](v4f &v) {
 #pragma unroll
-                    for (int u = 0; u < NU; ++u) f(dst + 16 * u, y[u][t], len - (n + 16 * u + 4 * q));
+                          for (int e = 0; e < 4; ++e)
+                              if (e < left) v[e] = at[e];
+                      },
+                      [&](const v4f &v) {
+#pragma unroll
+                          for (int e = 0; e < 4; ++e)
+                              if (e < left) at[e] = v[e];
+                      });
                 }
             }
         };
-        auto read = [](const float *src, v4f &v, int left) {
-            if constexpr (YVEC) {
-                if (left > 0) v = *reinterpret_cast<const v4f *>(src);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) v[e] = src[e];
-            }
-        };
-        auto write = [](float *dst, const v4f &v, int left) {
-            if constexpr (YVEC) {
-                if (left > 0) *reinterpret_cast<v4f *>(dst) = v;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) dst[e] = v[e];
-            }
-        };
-        int n = wave * (16 * NU);
+        auto read = [&](int i, int, auto get, auto) { get(y[i]); };
+        int n = 0;
         load_b(n);  // (in flight while S is summed)
         each_y(n, read);
         const float scale = a.scales ? a.scales[cur] : 1.0f;
@@ -295,9 +403,16 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
             v4f s = v4f{0.f, 0.f, 0.f, 0.f};
             if ((match >> m & 1) && j < rank) {
                 const float *src = a.ws + (m0 + m) * p.rp + j;
-#pragma unroll 4
-                for (int k = 0; k < p.splits; ++k, src += part)
-                    s += *reinterpret_cast<const v4f *>(src);
+                for (int k = 0; k < p.splits; k += 8) {  // (eight parts' loads at a time)
+                    v4f v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (k + e < p.splits)
+                            v[e] = *reinterpret_cast<const v4f *>(src + (k + e) * part);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (k + e < p.splits) s += v[e];
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] = j + e < rank ? s[e] : 0.0f;
             }
@@ -328,43 +443,59 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
                         for (int i = 2; i >= 0; --i)
                             acc = mfma(__builtin_bit_cast(v8bf, VEC ? and8(w[u][s], keep[s]) : w[u][s]),
                                        f[t][s][i], acc);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[u][t][e] = __builtin_fmaf(scale, acc[e], y[u][t][e]);
+                    *reinterpret_cast<v4f *>(&D[16 * t + c16][64 * wave + 16 * u + 4 * q]) = acc;
                 }
             if (next < len) load_b(next);
-            each_y(n, write);
+            lds_barrier();
+            each_y(n, [&](int i, int m, auto, auto put) {
+                const v4f d = *reinterpret_cast<const v4f *>(&D[m][4 * lane]);
+                v4f v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(scale, d[e], y[i][e]);
+                put(v);
+            });
             if (next >= len) break;
             n = next;
             each_y(n, read);
+            lds_barrier();  // (D has been read)
         }
     });
+    }
 }
 
 // ------------------------------------------------------------------ launches
 constexpr int kMaxSplits = 16;
-constexpr int64_t kSplitRows = 32768;  // rows of S in the workspace beyond the first part, at most
+constexpr int64_t kSplitRows = 65536;  // rows of S in the workspace beyond the first part, at most
+
+// a tile's 32 rows lie within a descriptor's range
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 static int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
-// S in up to 1 + min(15, 32768 / M) parts: the size grows with M and rank alone.
+// S in up to 1 + min(15, 65536 / M) parts: the size grows with M and rank alone.
 size_t lora_ws_bytes(int64_t M, int64_t, int64_t, int64_t rank) {
     const int64_t rows = M + std::min(M * (kMaxSplits - 1), kSplitRows);
     return (size_t)rows * (size_t)round16(rank) * 4;
 }
 
-template <bool FP32, bool VEC, int MT>
-static void go_down(const LoraArgs &a, const LoraPlan &p, int64_t tiles, hipStream_t st) {
-    const int rc = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
-    const dim3 g((unsigned)(tiles * p.slots), (unsigned)p.splits,
-                 (unsigned)((a.rank + 16 * rc - 1) / (16 * rc)));
-    if (rc == 1) launch_kv(k_lora_down<FP32, VEC, MT, 1>, g, dim3(256), 0, st, a, p);
-    else if (rc == 2) launch_kv(k_lora_down<FP32, VEC, MT, 2>, g, dim3(256), 0, st, a, p);
-    else launch_kv(k_lora_down<FP32, VEC, MT, 4>, g, dim3(256), 0, st, a, p);
+template <bool FP32, int MT, int RC>
+static void go_down_as(const LoraArgs &a, const LoraPlan &p, bool vec, hipStream_t st) {
+    const dim3 g((unsigned)p.splits, (unsigned)std::min<int64_t>((int64_t)p.tiles * p.slots, 65535),
+                 (unsigned)((a.rank + 16 * RC - 1) / (16 * RC)));
+    if (vec) launch_kv(k_lora_down_lds<FP32, MT, RC>, g, dim3(256), 0, st, a, p);
+    else launch_kv(k_lora_down<FP32, MT, RC>, g, dim3(256), 0, st, a, p);
+}
+
+template <bool FP32, int MT>
+static void go_down(const LoraArgs &a, const LoraPlan &p, bool vec, hipStream_t st) {
+    if (a.rank <= 16) go_down_as<FP32, MT, 1>(a, p, vec, st);
+    else if (a.rank <= 32) go_down_as<FP32, MT, 2>(a, p, vec, st);
+    else go_down_as<FP32, MT, 4>(a, p, vec, st);
 }
 
 template <bool VEC, bool YVEC, int MT>
-static void go_up(const LoraArgs &a, const LoraPlan &p, int64_t tiles, hipStream_t st) {
-    const dim3 g((unsigned)(tiles * p.slots), (unsigned)((a.N + p.nc - 1) / p.nc));
+static void go_up(const LoraArgs &a, const LoraPlan &p, hipStream_t st) {
+    const dim3 g((unsigned)((a.N + p.nc - 1) / p.nc), (unsigned)std::min<int64_t>((int64_t)p.tiles * p.slots, 65535));
     if (a.rank <= 32) launch_kv(k_lora_up<VEC, YVEC, MT, 1>, g, dim3(256), 0, st, a, p);
     else if (a.rank <= 64) launch_kv(k_lora_up<VEC, YVEC, MT, 2>, g, dim3(256), 0, st, a, p);
     else if (a.rank <= 128) launch_kv(k_lora_up<VEC, YVEC, MT, 4>, g, dim3(256), 0, st, a, p);
@@ -383,23 +514,24 @@ static void go(const LoraArgs &a, hipStream_t st) {
     LoraPlan p{};
     p.rp = (int)round16(a.rank);
     int64_t splits = std::min<int64_t>(1 + std::min<int64_t>(kMaxSplits - 1, kSplitRows / a.M),
-                                       std::min<int64_t>((a.K + 511) / 512, (1024 + tiles - 1) / tiles));
+                                       std::min<int64_t>((a.K + 511) / 512, (2048 + tiles - 1) / tiles));
     p.kc = (int)(((a.K + splits - 1) / splits + 127) / 128 * 128);
     p.splits = (int)((a.K + p.kc - 1) / p.kc);
     p.slots = slots(tiles * p.splits);
-    const bool xv = a.K % 8 == 0 && at16(a.X) && at16(a.A) && a.ldx * (a.fp32 ? 4 : 2) % 16 == 0;
-    if (a.fp32) xv ? go_down<true, true, MT>(a, p, tiles, st) : go_down<true, false, MT>(a, p, tiles, st);
-    else xv ? go_down<false, true, MT>(a, p, tiles, st) : go_down<false, false, MT>(a, p, tiles, st);
+    p.tiles = (int)tiles;
+    const bool xv = a.K % 8 == 0 && at16(a.X) && at16(a.A) && a.ldx * (a.fp32 ? 4 : 2) % 16 == 0 &&
+                    a.ldx <= kMaxStride;
+    a.fp32 ? go_down<true, MT>(a, p, xv, st) : go_down<false, MT>(a, p, xv, st);
 
     const bool bv = a.rank % 8 == 0 && at16(a.B);
     const bool yv = a.N % 4 == 0 && a.ldy % 4 == 0 && at16(a.Y);
     const int64_t chunks = (a.N + 255) / 256;
-    const int64_t per = std::max<int64_t>(
-        std::max<int64_t>(1, std::min<int64_t>(4, tiles * chunks / 2048)), (chunks + 65534) / 65535);
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(
+        MT == 1 ? 4 : 2, tiles * std::min<int64_t>(16 * MT, a.adapters) * chunks / 448));
     p.nc = (int)(256 * per);
     p.slots = slots(tiles * ((a.N + p.nc - 1) / p.nc));
-    if (bv) yv ? go_up<true, true, MT>(a, p, tiles, st) : go_up<true, false, MT>(a, p, tiles, st);
-    else yv ? go_up<false, true, MT>(a, p, tiles, st) : go_up<false, false, MT>(a, p, tiles, st);
+    if (bv) yv ? go_up<true, true, MT>(a, p, st) : go_up<true, false, MT>(a, p, st);
+    else yv ? go_up<false, true, MT>(a, p, st) : go_up<false, false, MT>(a, p, st);
 }
 
 hipError_t launch_lora(const LoraArgs &a, const char **path, hipStream_t st) {

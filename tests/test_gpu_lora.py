@@ -248,3 +248,23 @@ def test_captured_and_on_another_stream(M):
             torch.cuda.synchronize()
             assert torch.equal(out[i], want)
             w4.lora_add(base[:1].clone(), X[:1], ids[:1], A, B, workspace=work)
+
+
+@pytest.mark.parametrize("M,N,L", [(1200007, 8, 3), (2100001, 4, 1), (2, 1200000, 2)])
+def test_many_rows_or_channels(M, N, L):
+    """More tiles than a grid dimension holds, and a long row."""
+    K, r = 8, 8
+    g = torch.Generator(device="cuda").manual_seed(M)
+    X = torch.randn((M, K), generator=g, device="cuda")
+    A = torch.randn((L, r, K), generator=g, device="cuda").bfloat16()
+    B = torch.randn((L, N, r), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    Y = torch.randn((M, N), generator=g, device="cuda")
+    y = w4.lora_add(Y.clone(), X, ids, A, B)
+    low = (X.double() @ A.double().view(L * r, K).T).view(M, L, r)
+    mag = (X.double().abs() @ A.double().abs().view(L * r, K).T).view(M, L, r)
+    take = (ids[:, None] == torch.arange(L, device="cuda"))[..., None]
+    Bd = B.double().transpose(1, 2).reshape(L * r, N)
+    d = torch.where(take, low, 0.0).view(M, -1) @ Bd
+    e = torch.where(take, mag, 0.0).view(M, -1) @ Bd.abs()
+    assert ((y.double() - Y.double() - d).abs() <= (K + r + 64) * U * e + 2 * U * (Y.double().abs() + d.abs())).all()
