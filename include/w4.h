@@ -543,7 +543,7 @@ typedef enum { RMS_BF16 = 0, RMS_FP32 = 1 } rms_dtype;
  *            before); required with a residual, NULL without.  It may be the
  *            residual itself, or x itself where x_stride is K;
  *   out      [M][K] of out_dtype; it overlaps nothing else.
- * eps is finite and not below 0.  1 <= K <= W4_MAX_K, 1 <= M <= 2^23.
+ * eps is finite and not below 0.  1 <= K <= W4_MAX_K, 1 <= M <= 2^23, M * K <= 2^36.
  * Since h^2 is exact in fp64 and the mean is rounded far below fp32, the result
  * does not depend on the order of the sum: every kernel gives the same bits.
  * A row with a value that is not finite gives what the formula gives for it

@@ -15,6 +15,7 @@ namespace {
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 23;     // a grid has fewer than 2^32 threads, 256 a row
+constexpr int64_t kMaxNorm = (int64_t)1 << 36;     // values of a norm: 512 or 1024 threads a long row
 constexpr int64_t kMaxVectors = (int64_t)1 << 26;  // (token, head) pairs of a call
 constexpr int64_t kMaxValues = (int64_t)1 << 46;   // of one array, strides included
 constexpr int64_t kMaxAdapters = (int64_t)1 << 20;
@@ -37,7 +38,7 @@ int norm(const void *x, int x_dtype, int64_t ldx, const void *res, const float *
         return W4_ERR_NULL;
     if (!x_type(x_dtype) || !std::isfinite(offset) || !std::isfinite(eps) || eps < 0.0f)
         return W4_ERR_ARG;
-    if (M < 1 || K < 1 || M > kMaxRows || K > W4_MAX_K || !rows_ok(M, K, ldx))
+    if (M < 1 || K < 1 || M > kMaxRows || K > W4_MAX_K || M > kMaxNorm / K || !rows_ok(M, K, ldx))
         return W4_ERR_SHAPE;
     const size_t e = x_size(x_dtype);
     const size_t o = out_type == w4::kNormInt8 ? 1 : out_type == RMS_FP32 ? 4 : 2;

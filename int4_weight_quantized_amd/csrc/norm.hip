@@ -6,10 +6,14 @@
 // below fp32's, so r, and with it every code next to a rounding border, is the
 // same whichever way a row is split over lanes.  Bound by memory: a row is read
 // once, kept in registers between the sum and the output, and written once.
+#include <type_traits>
+
 #include "kv_common.h"
 #include "layer.h"
 
 namespace w4 {
+
+template <int N> using Int = std::integral_constant<int, N>;
 
 // ------------------------------------------------------------------ helpers
 __device__ __forceinline__ double dpp_double(double v, int which) {
@@ -81,13 +85,13 @@ __device__ __forceinline__ float row_scale_of(uint32_t m, uint32_t *red) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 
-// Any K, stride and alignment: the row is read twice (the second time from the
-// caches) a value at a time.  A value's sum is written by the thread that has
+// Rows longer than registers hold: read again from the caches for the scale and
+// the output, a value at a time.  A value's sum is written by the thread that has
 // read it, in the second pass, so that the sum may be the residual or x.
 template <bool FP32, int OUT>
-__global__ __launch_bounds__(256) void k_rms_norm_any(NormArgs a) {
-    __shared__ double red[4];
-    __shared__ uint32_t redm[4];
+__global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
+    __shared__ double red[16];
+    __shared__ uint32_t redm[16];
     const int64_t m = blockIdx.x, K = a.K;
     auto value = [&](const void *p, int64_t at) {
         if constexpr (FP32) return reinterpret_cast<const float *>(p)[at];
@@ -98,21 +102,21 @@ __global__ __launch_bounds__(256) void k_rms_norm_any(NormArgs a) {
         return a.res ? x + value(a.res, m * K + k) : x;
     };
     double ss = 0.0;
-    for (int64_t k = threadIdx.x; k < K; k += 256) {
+    for (int64_t k = threadIdx.x; k < K; k += 1024) {
         const double d = h(k);
         ss = __builtin_fma(d, d, ss);
     }
-    const float r = row_rsqrt<4>(ss, red, K, a.eps);
+    const float r = row_rsqrt<16>(ss, red, K, a.eps);
     auto y = [&](int64_t k, float v) { return (v * r) * (a.offset + (a.weight ? a.weight[k] : 1.0f)); };
     float s = 0.0f;
     if constexpr (OUT == kNormInt8) {
         uint32_t top = 0;
-        for (int64_t k = threadIdx.x; k < K; k += 256) top = max(top, abs_bits(y(k, h(k))));
-        s = row_scale_of<4>(top, redm);
+        for (int64_t k = threadIdx.x; k < K; k += 1024) top = max(top, abs_bits(y(k, h(k))));
+        s = row_scale_of<16>(top, redm);
         if (threadIdx.x == 0) a.sx[m] = s;
     }
     const RowScale q = row_scale(s);
-    for (int64_t k = threadIdx.x; k < K; k += 256) {
+    for (int64_t k = threadIdx.x; k < K; k += 1024) {
         const float v = h(k), f = y(k, v);
         if (a.sum) {
             if constexpr (FP32) reinterpret_cast<float *>(a.sum)[m * K + k] = v;
@@ -125,18 +129,186 @@ __global__ __launch_bounds__(256) void k_rms_norm_any(NormArgs a) {
     }
 }
 
-template <bool FP32>
-static void go(const NormArgs &a, hipStream_t st) {
-    const dim3 g((unsigned)a.M), b(256);
-    if (a.out_type == kNormInt8) launch_kv(k_rms_norm_any<FP32, kNormInt8>, g, b, 0, st, a);
-    else if (a.out_type == RMS_FP32) launch_kv(k_rms_norm_any<FP32, RMS_FP32>, g, b, 0, st, a);
-    else launch_kv(k_rms_norm_any<FP32, RMS_BF16>, g, b, 0, st, a);
+// Pieces of 16 bytes of x (V = 4 or 8 values), or single values (V = 1) where K, a
+// stride or an address does not allow those: thread t owns pieces t, t + T, ... (NG), all loads issued at once, neighbouring lanes side by
+// side in every array; a row is read once and stays in registers.  x and the
+// residual are read, and the sum written, past the caches, whose place the output
+// has for the product that takes it (8192 rows of 8192, fp32 with residual to bf16,
+// 940 MB: 152 us, 6.2 TB/s; 163 us with all of it through the caches).
+template <bool FP32, int V>
+__device__ __forceinline__ void load_piece(const void *p, int64_t at, float (&f)[V]) {
+    if constexpr (V == 1) {
+        if constexpr (FP32) f[0] = reinterpret_cast<const float *>(p)[at];
+        else f[0] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[at] << 16);
+    } else if constexpr (FP32) {
+        const v4f *s = reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(p) + at);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const v4f a = __builtin_nontemporal_load(s + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * i + j] = a[j];
+        }
+    } else {
+        const u32x4 w = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p) + at));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+    }
+}
+
+template <bool FP32, bool KEEP, int V>
+__device__ __forceinline__ void store_piece(void *p, int64_t at, const float (&f)[V]) {
+    auto put = [](auto v, auto *o) {
+        if constexpr (KEEP || V == 1) *o = v;
+        else __builtin_nontemporal_store(v, o);
+    };
+    if constexpr (V == 1) {
+        if constexpr (FP32) put(f[0], reinterpret_cast<float *>(p) + at);
+        else put((uint16_t)pack_bf16(f[0], 0.0f), reinterpret_cast<uint16_t *>(p) + at);
+    } else if constexpr (FP32) {
+        v4f *o = reinterpret_cast<v4f *>(reinterpret_cast<float *>(p) + at);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            put(v4f{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}, o + i);
+    } else {
+        typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+        words w;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+        put(w, reinterpret_cast<words *>(reinterpret_cast<uint16_t *>(p) + at));
+    }
+}
+
+template <bool FP32, int OUT, bool RES, int V, int T, int NG>
+__global__ __launch_bounds__(T) void k_rms_norm(NormArgs a) {
+    constexpr int kWaves = T / kWave;
+    __shared__ double red[kWaves];
+    __shared__ uint32_t redm[kWaves];
+    const int64_t m = blockIdx.x, K = a.K;
+    const int ng = (int)K / V;
+    float h[NG][V], r[NG][V], w[NG][V];
+#pragma unroll
+    for (int u = 0; u < NG; ++u) {
+        const int g = threadIdx.x + T * u;
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[u][j] = 0.0f, r[u][j] = 0.0f, w[u][j] = 1.0f;
+        if (g >= ng) continue;
+        load_piece<FP32>(a.x, m * a.ldx + V * g, h[u]);
+        if constexpr (RES) load_piece<FP32>(a.res, m * K + V * g, r[u]);
+        if (a.weight) {
+            if constexpr (V == 1) w[u][0] = a.weight[g];
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 p = reinterpret_cast<const float4 *>(a.weight + V * g)[i];
+                w[u][4 * i] = p.x, w[u][4 * i + 1] = p.y, w[u][4 * i + 2] = p.z, w[u][4 * i + 3] = p.w;
+            }
+        }
+    }
+    double ss = 0.0;
+#pragma unroll
+    for (int u = 0; u < NG; ++u) {
+        const int g = threadIdx.x + T * u;
+        if constexpr (RES) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[u][j] += r[u][j];
+            if (g < ng) store_piece<FP32, false>(a.sum, m * K + V * g, h[u]);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const double d = h[u][j];
+            ss = __builtin_fma(d, d, ss);
+        }
+    }
+    const float s = row_rsqrt<kWaves>(ss, red, K, a.eps);
+#pragma unroll
+    for (int u = 0; u < NG; ++u)
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[u][j] = (h[u][j] * s) * (a.offset + w[u][j]);
+    if constexpr (OUT == kNormInt8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < NG; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (threadIdx.x + T * u < ng) top = max(top, abs_bits(h[u][j]));
+        const float sx = row_scale_of<kWaves>(top, redm);
+        if (threadIdx.x == 0) a.sx[m] = sx;
+        auto codes = [&](auto code) {
+#pragma unroll
+            for (int u = 0; u < NG; ++u) {
+                const int g = threadIdx.x + T * u;
+                if (g >= ng) continue;
+                int8_t *o = reinterpret_cast<int8_t *>(a.out) + m * K + V * g;
+                const float(&f)[V] = h[u];
+                if constexpr (V == 1) {
+                    *o = (int8_t)code(f[0]);
+                } else {
+                    uint32_t c[V / 4];
+#pragma unroll
+                    for (int i = 0; i < V / 4; ++i)
+                        c[i] = pack4_i8(code(f[4 * i]), code(f[4 * i + 1]), code(f[4 * i + 2]),
+                                        code(f[4 * i + 3]));
+                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(o) = uint2{c[0], c[1]};
+                    else *reinterpret_cast<uint32_t *>(o) = c[0];
+                }
+            }
+        };
+        if (sx >= kFastQuotientMinScale) {
+            const float rs = 1.0f / sx;
+            codes([&](float x) { return (int)code_in_low_byte(quotient_rn(x, sx, rs)); });
+        } else {  // zero, tiny or NaN
+            const RowScale q = row_scale(sx);
+            codes([&](float x) { return quant_code_row(x, q); });
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < NG; ++u) {
+            const int g = threadIdx.x + T * u;
+            if (g < ng) store_piece<OUT == RMS_FP32, true>(a.out, m * K + V * g, h[u]);
+        }
+    }
+}
+
+template <bool FP32, int OUT>
+static void launch_as(const NormArgs &a, const char **path, hipStream_t st) {
+    auto at = [](const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+    constexpr int V = FP32 ? 4 : 8;
+    const bool whole = a.K % V == 0 && a.ldx % V == 0 && at(a.x, 16) && at(a.res, 16) &&
+                       at(a.sum, 16) && at(a.weight, 16) &&
+                       at(a.out, OUT == kNormInt8 ? V : OUT == RMS_FP32 ? 16 : 2 * V);
+    const dim3 g((unsigned)a.M);
+    auto go = [&](auto v, auto t, auto values) {
+        constexpr int P = decltype(v)::value, T = decltype(t)::value;
+        constexpr int NG = decltype(values)::value / P;
+        *path = P > 1 ? "rms_norm" : "rms_norm_odd";
+        if (a.res) launch_kv(k_rms_norm<FP32, OUT, true, P, T, NG>, g, dim3(T), 0, st, a);
+        else launch_kv(k_rms_norm<FP32, OUT, false, P, T, NG>, g, dim3(T), 0, st, a);
+    };
+    auto run = [&](auto t, auto values) { go(Int<V>{}, t, values); };
+    // Up to 32 values a thread, and the fewest threads that this allows: they meet at
+    // fewer barriers (8192 rows of 8192, us: 256 / 512 / 1024 threads 151 / 156 / 153;
+    // 64 rows of 4096: 3.6 / 3.6 / 5.2).
+    if (whole && a.K <= 2048) return run(Int<256>{}, Int<8>{});
+    if (whole && a.K <= 4096) return run(Int<256>{}, Int<16>{});
+    if (whole && a.K <= 8192) return run(Int<256>{}, Int<32>{});
+    if (whole && a.K <= 16384) return run(Int<512>{}, Int<32>{});
+    if (whole && a.K <= 32768) return run(Int<1024>{}, Int<32>{});
+    if (!whole && a.K <= 8192) return go(Int<1>{}, Int<256>{}, Int<32>{});
+    if (!whole && a.K <= 16384) return go(Int<1>{}, Int<512>{}, Int<32>{});
+    if (!whole && a.K <= 32768) return go(Int<1>{}, Int<1024>{}, Int<32>{});
+    *path = "rms_norm_long";
+    launch_kv(k_rms_norm_long<FP32, OUT>, g, dim3(1024), 0, st, a);
 }
 
 hipError_t launch_rms_norm(const NormArgs &a, const char **path, hipStream_t st) {
-    *path = "rms_norm";
-    if (a.fp32) go<true>(a, st);
-    else go<false>(a, st);
+    auto type = [&](auto fp32) {
+        constexpr bool F = decltype(fp32)::value;
+        if (a.out_type == kNormInt8) launch_as<F, kNormInt8>(a, path, st);
+        else if (a.out_type == RMS_FP32) launch_as<F, RMS_FP32>(a, path, st);
+        else launch_as<F, RMS_BF16>(a, path, st);
+    };
+    if (a.fp32) type(std::true_type{});
+    else type(std::false_type{});
     return hipGetLastError();
 }
 

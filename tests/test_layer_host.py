@@ -37,7 +37,7 @@ def norm8(**kw):
     (dict(eps=INF), ARG), (dict(offset=NAN), ARG), (dict(offset=-INF), ARG),
     (dict(M=0), SHAPE), (dict(K=0), SHAPE), (dict(M=-1), SHAPE), (dict(ldx=63), SHAPE),
     (dict(M=(1 << 23) + 1), SHAPE), (dict(K=w4.W4_MAX_K + 1, ldx=1 << 18), SHAPE),
-    (dict(ldx=1 << 46), SHAPE), (dict(ldx=-64), SHAPE),
+    (dict(ldx=1 << 46), SHAPE), (dict(ldx=-64), SHAPE), (dict(M=1 << 22, K=16385, ldx=16385), SHAPE),
     (dict(x=FAKE + 2), ALIGN), (dict(res=FAKE + 2), ALIGN), (dict(sum=FAKE + 1), ALIGN),
     (dict(w=FAKE + 2), ALIGN)])
 def test_norm_refusals(kw, rc):
