@@ -5,111 +5,195 @@
 //   c, s = fp32 of magnitude * cos, sin(2 pi t).
 // Angles are taken in fp64: p turns[i] loses 2^-53 of itself, so that a token at
 // position 10^6 still has its angle to 10^-10 where fp32 would be off by a tenth
-// of a turn, and c and s are rounded once.  A token's angles are computed once
-// by its workgroup, for all of its heads.
+// of a turn, and c and s are rounded once.
+//
+// A wave takes one token: it computes the token's angles (64 at once), keeps those
+// of its lanes' values in registers, and goes through the token's heads, 1 KB at a
+// time, four loads ahead; waves share nothing.  Calls of few tokens split a
+// token's heads over several waves, each with the angles.  Bound by memory.
+#include <algorithm>
+#include <type_traits>
+
 #include "kv_common.h"
 #include "layer.h"
 
 namespace w4 {
 
-constexpr int kTokens = 4;     // of a workgroup, at most
-constexpr int kHalf = 256;     // pairs of a token, at most
+constexpr int kHalf = 256;  // pairs of a token, at most
+constexpr int kAhead = 4;   // loads of a lane in flight
 
+template <int N> using Int = std::integral_constant<int, N>;
+
+// Memory of one wave.
 struct RopeLds {
-    float2 cs[kTokens * kHalf];
-    float4 swap[2][256];
+    float2 cs[kHalf];
+    float4 swap[kWave * 2];
 };
 
-// Angles of a workgroup's tokens at positions pos[0 .. n - 1] (LDS).
-__device__ __forceinline__ void rope_angles(const RopeView &r, const int64_t *pos, int n,
-                                            float2 *cs) {
-    for (int i = threadIdx.x; i < n * r.half; i += 256) {
-        const int t = i / r.half;
-        const double turns = (double)pos[t] * r.turns[i - t * r.half];
+// LDS of a wave is read in the order in which it was written; this keeps the
+// compiler to it.
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// The factors of the V values d, d + 1, ... of a head that this lane holds.
+template <int V>
+struct Turn {
+    float c[V], s[V];  // value * c + other * s
+    int rot;           // how many of them turn
+    int other;         // first value of the partners' 16-byte piece (half layout), or -1
+    int d;
+};
+
+template <int V>
+__device__ __forceinline__ Turn<V> rope_turn(const RopeView &r, int64_t pos, int d, RopeLds &l) {
+    for (int i = threadIdx.x % kWave; i < r.half; i += kWave) {
+        const double turns = (double)pos * r.turns[i];
         double s, c;
         sincospi(2.0 * (turns - rint(turns)), &s, &c);
-        cs[i] = float2{(float)(r.magnitude * c), (float)(r.magnitude * s)};
+        l.cs[i] = float2{(float)(r.magnitude * c), (float)(r.magnitude * s)};
     }
+    wave_fence();
+    Turn<V> t;
+    t.d = d;
+    t.rot = r.rot - d;
+    t.other = r.half % V == 0 && d < r.rot ? (d < r.half ? d + r.half : d - r.half) : -1;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = min(d + j, r.rot - 1);
+        const bool low = r.pairs ? e % 2 == 0 : e < r.half;
+        const float2 u = l.cs[r.pairs ? e / 2 : low ? e : e - r.half];
+        t.c[j] = u.x;
+        t.s[j] = low ? -u.y : u.y;
+    }
+    return t;
 }
 
-// Rotate the 8 values d, d + 1, ... of a head that this lane holds; the other
-// half of a pair is another lane's of the same wave, which hands it over in LDS.
-__device__ __forceinline__ void rotate8(const RopeView &r, const float2 *cs, int d, float4 (*swap)[256],
-                                        float (&f)[8]) {
+// Rotate f.  In the half layout the other value of a pair is another lane's of the
+// same head, `group` lanes that start at lane `first` of the wave; it goes through LDS.
+template <int V>
+__device__ __forceinline__ void rotate(const RopeView &r, const Turn<V> &t, int first, float4 *swap,
+                                       float (&f)[V]) {
+    float o[V];
     if (r.pairs) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            if (d + j >= r.rot) continue;
-            const float2 u = cs[(d + j) / 2];
-            const float a = f[j], b = f[j + 1];
-            f[j] = a * u.x - b * u.y;
-            f[j + 1] = b * u.x + a * u.y;
-        }
-        return;
-    }
-    swap[0][threadIdx.x] = float4{f[0], f[1], f[2], f[3]};
-    swap[1][threadIdx.x] = float4{f[4], f[5], f[6], f[7]};
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int first = threadIdx.x - d / 8;  // the lane of the head's value 0
+        for (int j = 0; j < V; ++j) o[j] = f[j ^ 1];
+    } else {
+        const int lane = threadIdx.x % kWave;
+        const float *from = reinterpret_cast<const float *>(swap) + first * V;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = d + j;
-        if (e >= r.rot) continue;
-        const bool low = e < r.half;
-        const int o = low ? e + r.half : e - r.half;
-        const float other =
-            reinterpret_cast<const float *>(&swap[(o >> 2) & 1][first + (o >> 3)])[o & 3];
-        const float2 u = cs[low ? e : o];
-        f[j] = low ? f[j] * u.x - other * u.y : f[j] * u.x + other * u.y;
+        for (int i = 0; i < V / 4; ++i)
+            swap[lane * (V / 4) + i] = float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+        wave_fence();
+        if (r.half % V == 0) {
+            const int at = max(t.other, 0);
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + at + 4 * i);
+                o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = min(t.d + j, r.rot - 1);
+                o[j] = from[e < r.half ? e + r.half : e - r.half];
+            }
+        }
+        wave_fence();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float y = f[j] * t.c[j] + o[j] * t.s[j];
+        f[j] = j < t.rot ? y : f[j];
+    }
 }
 
-template <bool FP32>
-__device__ __forceinline__ void store8(void *x, int64_t at, bool vec, const float (&f)[8]) {
+template <bool FP32, int V>
+__device__ __forceinline__ void load_values(const void *x, int64_t at, bool vec, float (&f)[V]) {
+    if constexpr (FP32) {
+        const float *s = reinterpret_cast<const float *>(x) + at;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const v4f v = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(s) + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[4 * i + j] = v[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] = s[j];
+        }
+    } else {
+        const uint16_t *s = reinterpret_cast<const uint16_t *>(x) + at;
+        if (vec) {
+            const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s));
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] = __uint_as_float((uint32_t)s[j] << 16);
+        }
+    }
+}
+
+template <bool FP32, int V>
+__device__ __forceinline__ void store_values(void *x, int64_t at, bool vec, const float (&f)[V]) {
     if constexpr (FP32) {
         float *o = reinterpret_cast<float *>(x) + at;
         if (vec) {
-            reinterpret_cast<float4 *>(o)[0] = float4{f[0], f[1], f[2], f[3]};
-            reinterpret_cast<float4 *>(o)[1] = float4{f[4], f[5], f[6], f[7]};
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i)
+                reinterpret_cast<v4f *>(o)[i] = v4f{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = f[j];
+            for (int j = 0; j < V; ++j) o[j] = f[j];
         }
     } else {
         uint16_t *o = reinterpret_cast<uint16_t *>(x) + at;
-        const uint4 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+        const u32x4 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
                          pack_bf16(f[6], f[7])};
         if (vec) {
-            *reinterpret_cast<uint4 *>(o) = w;
+            *reinterpret_cast<u32x4 *>(o) = w;
         } else {
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = (uint16_t)(u[j / 2] >> (j % 2 * 16));
+            for (int j = 0; j < V; ++j) o[j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
         }
     }
 }
 
-// LPV lanes a head, 8 values a lane.
-template <bool FP32, int LPV>
-__global__ __launch_bounds__(256) void k_rope(RopeArgs a, bool vec) {
-    __shared__ RopeLds lds;
-    __shared__ int64_t pos[kTokens];
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-    const int n = (int)min((int64_t)kTokens, a.T - t0);
-    if (threadIdx.x < n) pos[threadIdx.x] = a.pos[t0 + threadIdx.x];
-    __syncthreads();
-    rope_angles(a.rope, pos, n, lds.cs);
-    __syncthreads();
-    const int d = threadIdx.x % LPV * 8;
-    for (int i = 0; i < n * a.heads; i += 256 / LPV) {
-        const int v = i + threadIdx.x / LPV;
-        const int t = v / a.heads, h = v - t * a.heads;
-        const bool on = t < n && d < a.D;
-        float f[8] = {};
-        if (on) load8<FP32>(a.x, (t0 + t) * a.ldx + (int64_t)h * a.D + d, vec, f);
-        rotate8(a.rope, lds.cs + min(t, n - 1) * a.rope.half, d, lds.swap, f);
-        if (on) store8<FP32>(a.out, (t0 + t) * a.ldo + (int64_t)h * a.D + d, vec, f);
+// LPV lanes a head, V values a lane; `parts` waves a token.
+template <bool FP32, int V, int LPV>
+__global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts, bool vec) {
+    __shared__ RopeLds lds[4];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave, d = lane % LPV * V, first = lane / LPV * LPV;
+    const uint32_t unit = blockIdx.x * 4 + wave;
+    const int64_t row = unit / (uint32_t)parts;
+    if (row >= a.T) return;
+    const int per = (a.heads + kWave / LPV - 1) / (kWave / LPV);  // pieces of the token
+    const int step = (per + parts - 1) / parts;
+    const int i0 = (int)(unit % (uint32_t)parts) * step, i1 = min(i0 + step, per);
+    const int64_t from = row * a.ldx, to = row * a.ldo;
+    float f[kAhead][V];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = (i + u) * (kWave / LPV) + lane / LPV;
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[u][j] = 0.0f;
+            if (i + u < i1 && h < a.heads && d < a.D)
+                load_values<FP32>(a.x, from + h * a.D + d, vec, f[u]);
+        }
+    };
+    load(i0);  // (in flight while the angles are computed)
+    const Turn<V> t = rope_turn<V>(a.rope, a.pos[row], d, lds[wave]);
+    for (int i = i0; i < i1; i += kAhead) {
+        if (i > i0) load(i);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (i + u >= i1) break;
+            const int h = (i + u) * (kWave / LPV) + lane / LPV;
+            rotate<V>(a.rope, t, first, lds[wave].swap, f[u]);
+            if (h < a.heads && d < a.D) store_values<FP32>(a.out, to + h * a.D + d, vec, f[u]);
+        }
     }
 }
 
@@ -134,45 +218,109 @@ __device__ __forceinline__ TokenPlace token_place(const KvView &c, const KvRows 
                           : (((int64_t)page * c.heads) << c.shift) + (pos & ((1 << c.shift) - 1))};
 }
 
-template <bool INT8, bool FP32, int LPV>
-__global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, bool vecq, bool veckv) {
-    __shared__ RopeLds lds;
-    __shared__ int64_t pos[kTokens], at[kTokens];
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-    const int n = (int)min((int64_t)kTokens, a.rows.T - t0);
-    const int wave = threadIdx.x / kWave;
-    if (wave < n) {
-        const TokenPlace p = token_place(a.c, a.rows, t0 + wave);
-        if (threadIdx.x % kWave == 0) pos[wave] = p.pos, at[wave] = p.at;
+// A head's vector into its place: bf16 half to even, or int8 by the cache's rule
+// (scale = absmax * fl(1 / 127), NaN for a vector that is not finite; the codes'
+// quotients are kv_store8's, correctly rounded without a division).
+template <bool INT8, int V, int LPV>
+__device__ __forceinline__ void cache_values(const KvView &c, bool isv, int64_t vec, int d, bool on,
+                                             const float (&f)[V]) {
+    uint8_t *pool = isv ? c.v : c.k;
+    if constexpr (INT8) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        m = max(m, (uint32_t)dpp<kQuadSwap1>((int)m));
+        m = max(m, (uint32_t)dpp<kQuadSwap2>((int)m));
+        m = max(m, (uint32_t)dpp<kRowHalfMirror>((int)m));
+        if constexpr (LPV > 8) m = max(m, (uint32_t)dpp<kRowMirror>((int)m));
+#pragma unroll
+        for (int o = 16; o < LPV; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
+        if (!on) return;
+        const float s = m < 0x7F800000u ? __uint_as_float(m) * (1.0f / 127.0f) : NAN;
+        uint32_t w[V / 4] = {};
+        auto codes = [&](auto code) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i)
+                w[i] = pack4_i8(code(f[4 * i]), code(f[4 * i + 1]), code(f[4 * i + 2]), code(f[4 * i + 3]));
+        };
+        if (s >= kFastQuotientMinScale) {
+            const float rs = 1.0f / s;
+            codes([&](float x) { return (int)code_in_low_byte(quotient_rn(x, s, rs)); });
+        } else {  // zero, tiny or NaN
+            codes([&](float x) { return quant_code(x, s, -128.0f, 127.0f); });
+        }
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(pool + vec * c.D + d) = uint2{w[0], w[1]};
+        else *reinterpret_cast<uint32_t *>(pool + vec * c.D + d) = w[0];
+        if (d == 0) (isv ? c.vs : c.ks)[vec] = s;
+    } else {
+        if (!on) return;
+        typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+        words w;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+        __builtin_nontemporal_store(w, reinterpret_cast<words *>(pool + (vec * c.D + d) * 2));
     }
-    __syncthreads();
-    rope_angles(a.rope, pos, n, lds.cs);
-    __syncthreads();
-    const int d = threadIdx.x % LPV * 8, D = a.c.D, heads = a.hq + 2 * a.c.heads;
-    for (int i = 0; i < n * heads; i += 256 / LPV) {
-        const int v = i + threadIdx.x / LPV;
-        const int t = min(v / heads, n - 1), h = v - v / heads * heads;
-        const bool isq = h < a.hq, isv = h >= a.hq + a.c.heads;
-        const int64_t row = t0 + t;
-        const int kh = isv ? h - a.hq - a.c.heads : h - a.hq;
-        const bool on = v < n * heads && d < D && pos[t] >= 0 && (isq || at[t] >= 0);
-        float f[8] = {};
-        if (on) {
-            if (isq) load8<FP32>(a.q, row * a.ldq + (int64_t)h * D + d, vecq, f);
-            else if (isv) load8<FP32>(a.v, row * a.ldv + (int64_t)kh * D + d, veckv, f);
-            else load8<FP32>(a.k, row * a.ldk + (int64_t)kh * D + d, veckv, f);
-        }
-        float g[8];
+}
+
+// The pieces of a token are those of its queries, then of its keys, then of its
+// values, each kind a whole number of pieces.
+template <bool INT8, bool FP32, int V, int LPV>
+__global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int parts, bool vecq,
+                                                        bool veckv) {
+    __shared__ RopeLds lds[4];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave, d = lane % LPV * V, first = lane / LPV * LPV;
+    const uint32_t unit = blockIdx.x * 4 + wave;
+    const int64_t row = unit / (uint32_t)parts;
+    if (row >= a.rows.T) return;
+    constexpr int kHeads = kWave / LPV;
+    const int D = a.c.D, heads = a.c.heads;
+    const int nq = (a.hq + kHeads - 1) / kHeads, nk = (heads + kHeads - 1) / kHeads;
+    const int per = nq + 2 * nk, step = (per + parts - 1) / parts;
+    const int i0 = (int)(unit % (uint32_t)parts) * step, i1 = min(i0 + step, per);
+    struct Piece {
+        const void *src;
+        int64_t at;
+        int kind, head, heads;  // 0: q, 1: k, 2: v
+        bool vec;
+    };
+    auto piece = [&](int i) {
+        if (i < nq) return Piece{a.q, row * a.ldq, 0, i * kHeads, a.hq, vecq};
+        if (i < nq + nk) return Piece{a.k, row * a.ldk, 1, (i - nq) * kHeads, heads, veckv};
+        return Piece{a.v, row * a.ldv, 2, (i - nq - nk) * kHeads, heads, veckv};
+    };
+    float f[kAhead][V];
+    auto load = [&](int i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = f[j];
-        rotate8(a.rope, lds.cs + t * a.rope.half, d, lds.swap, g);
+        for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = isv ? f[j] : g[j];
-        if (isq) {
-            if (on) store8<FP32>(a.out, row * a.ldo + (int64_t)h * D + d, vecq, f);
+            for (int j = 0; j < V; ++j) f[u][j] = 0.0f;
+            if (i + u >= i1) continue;
+            const Piece p = piece(i + u);
+            const int h = p.head + lane / LPV;
+            if (h < p.heads && d < D) load_values<FP32>(p.src, p.at + h * D + d, p.vec, f[u]);
         }
-        const int64_t vec = at[t] + ((int64_t)max(kh, 0) << a.c.shift);
-        kv_store8<INT8, LPV>(a.c, isv, vec, d, on && !isq, f);
+    };
+    load(i0);  // (in flight during the search for the place, and while the angles are computed)
+    const TokenPlace place = token_place(a.c, a.rows, row);
+    if (place.pos < 0) return;
+    const Turn<V> t = rope_turn<V>(a.rope, place.pos, d, lds[wave]);
+    for (int i = i0; i < i1; i += kAhead) {
+        if (i > i0) load(i);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (i + u >= i1) break;
+            const Piece p = piece(i + u);
+            const int h = p.head + lane / LPV;
+            const bool on = h < p.heads && d < D;
+            if (p.kind < 2) rotate<V>(a.rope, t, first, lds[wave].swap, f[u]);
+            if (p.kind == 0) {
+                if (on) store_values<FP32>(a.out, row * a.ldo + h * D + d, vecq, f[u]);
+            } else if (place.at >= 0) {
+                cache_values<INT8, V, LPV>(a.c, p.kind == 2, place.at + ((int64_t)h << a.c.shift), d,
+                                           on, f[u]);
+            }
+        }
     }
 }
 
@@ -180,14 +328,32 @@ static bool aligned16(const void *p, int64_t stride, bool fp32) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * (fp32 ? 4 : 2) % 16 == 0;
 }
 
+// Waves of a token: as many as its pieces, or 2048 of the call.
+static int parts_of(int64_t T, int pieces) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, 2048 / T));
+}
+
+// f(values of a lane, lanes of a head) for heads of D values: 16 bytes a lane, so
+// that neighbouring lanes read side by side, while a head fits a wave.
+template <bool FP32, typename F>
+static void by_head(int D, F f) {
+    constexpr int V = FP32 ? 4 : 8;
+    if (D <= 8 * V) f(Int<V>{}, Int<8>{});
+    else if (D <= 16 * V) f(Int<V>{}, Int<16>{});
+    else if (D <= 32 * V) f(Int<V>{}, Int<32>{});
+    else if (D <= 64 * V) f(Int<V>{}, Int<64>{});
+    else f(Int<8>{}, Int<64>{});
+}
+
 template <bool FP32>
 static void go_rope(const RopeArgs &a, hipStream_t st) {
-    const dim3 g((unsigned)((a.T + kTokens - 1) / kTokens)), b(256);
     const bool vec = aligned16(a.x, a.ldx, FP32) && aligned16(a.out, a.ldo, FP32);
-    if (a.D <= 64) launch_kv(k_rope<FP32, 8>, g, b, 0, st, a, vec);
-    else if (a.D <= 128) launch_kv(k_rope<FP32, 16>, g, b, 0, st, a, vec);
-    else if (a.D <= 256) launch_kv(k_rope<FP32, 32>, g, b, 0, st, a, vec);
-    else launch_kv(k_rope<FP32, 64>, g, b, 0, st, a, vec);
+    by_head<FP32>(a.D, [&](auto v, auto lanes) {
+        constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value;
+        const int parts = parts_of(a.T, (a.heads + kWave / LPV - 1) / (kWave / LPV));
+        launch_kv(k_rope<FP32, V, LPV>, dim3((unsigned)((a.T * parts + 3) / 4)), dim3(256), 0, st, a,
+                  parts, vec);
+    });
 }
 
 hipError_t launch_rope(const RopeArgs &a, hipStream_t st) {
@@ -198,12 +364,14 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t st) {
 
 template <bool INT8, bool FP32>
 static void go_append(const AppendRopeArgs &a, hipStream_t st) {
-    const dim3 g((unsigned)((a.rows.T + kTokens - 1) / kTokens)), b(256);
     const bool vecq = aligned16(a.q, a.ldq, FP32) && aligned16(a.out, a.ldo, FP32);
     const bool veckv = aligned16(a.k, a.ldk, FP32) && aligned16(a.v, a.ldv, FP32);
-    if (a.c.D <= 64) launch_kv(k_kv_append_rope<INT8, FP32, 8>, g, b, 0, st, a, vecq, veckv);
-    else if (a.c.D <= 128) launch_kv(k_kv_append_rope<INT8, FP32, 16>, g, b, 0, st, a, vecq, veckv);
-    else launch_kv(k_kv_append_rope<INT8, FP32, 32>, g, b, 0, st, a, vecq, veckv);
+    by_head<FP32>(a.c.D, [&](auto v, auto lanes) {
+        constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value, H = kWave / LPV;
+        const int parts = parts_of(a.rows.T, (a.hq + H - 1) / H + 2 * ((a.c.heads + H - 1) / H));
+        launch_kv(k_kv_append_rope<INT8, FP32, V, LPV>, dim3((unsigned)((a.rows.T * parts + 3) / 4)),
+                  dim3(256), 0, st, a, parts, vecq, veckv);
+    });
 }
 
 hipError_t launch_kv_append_rope(const AppendRopeArgs &a, hipStream_t st) {
