@@ -607,7 +607,7 @@ int rope_frequencies(int64_t rot_dim, double base, int scaling, double factor, i
  *   out  rows of the same values, out_stride apart; it may be x itself with the
  *        same stride, and overlaps it in no other way.  bf16: rounded once.
  * head_dim is a multiple of 8 up to 512, not below rot_dim; 1 <= T <= 2^23,
- * T * heads <= 2^26.
+ * heads <= 65535, T * heads <= 2^26.
  * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
 int rope_rotate(const rope_spec *rope, const void *x, int x_dtype, int64_t x_stride, int64_t T,
                 int64_t heads, int64_t head_dim, const int32_t *pos, void *out,

@@ -140,7 +140,7 @@ int rope_rotate(const rope_spec *rope, const void *x, int x_dtype, int64_t x_str
     if (!x || !pos || !out) return W4_ERR_NULL;
     if (!x_type(x_dtype)) return W4_ERR_ARG;
     if (head_dim > 512 || head_dim % 8 != 0 || T < 1 || T > kMaxRows || heads < 1 ||
-        heads > kMaxVectors / T || !rows_ok(T, heads * head_dim, x_stride) ||
+        heads > 65535 || heads > kMaxVectors / T || !rows_ok(T, heads * head_dim, x_stride) ||
         !rows_ok(T, heads * head_dim, out_stride))
         return W4_ERR_SHAPE;
     if (x == out && x_stride != out_stride) return W4_ERR_ARG;

@@ -106,81 +106,108 @@ __device__ __forceinline__ void rotate(const RopeView &r, const Turn<V> &t, int 
     }
 }
 
+// V values of a lane as they lie in memory, so that a load waits for nothing.
 template <bool FP32, int V>
-__device__ __forceinline__ void load_values(const void *x, int64_t at, bool vec, float (&f)[V]) {
-    if constexpr (FP32) {
-        const float *s = reinterpret_cast<const float *>(x) + at;
-        if (vec) {
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const v4f v = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(s) + i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[4 * i + j] = v[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = s[j];
-        }
-    } else {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(x) + at;
-        if (vec) {
-            const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s));
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = __uint_as_float((uint32_t)s[j] << 16);
-        }
-    }
-}
+struct Raw {
+    static constexpr int kSize = FP32 ? 4 : 2, kPieces = V * kSize / 16;
+    uint4 w[kPieces];
 
-template <bool FP32, int V>
-__device__ __forceinline__ void store_values(void *x, int64_t at, bool vec, const float (&f)[V]) {
-    if constexpr (FP32) {
-        float *o = reinterpret_cast<float *>(x) + at;
-        if (vec) {
+    // beyond the row's range: zeros
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i)
-                reinterpret_cast<v4f *>(o)[i] = v4f{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-        } else {
+        for (int i = 0; i < kPieces; ++i) w[i] = bload16_nt(r, (int)(at + 16 * i));
+    }
+    // the same for rows that are aligned to their elements only
+    __device__ __forceinline__ void load_some(const void *row, int at, bool on) {
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(row) + at;
+        uint32_t u[V * kSize / 4] = {};
+        if (on) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = f[j];
+            for (int j = 0; j < V; ++j) {
+                if constexpr (FP32) u[j] = reinterpret_cast<const uint32_t *>(p)[j];
+                else u[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (j % 2 * 16);
+            }
         }
-    } else {
-        uint16_t *o = reinterpret_cast<uint16_t *>(x) + at;
-        const u32x4 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7])};
-        if (vec) {
-            *reinterpret_cast<u32x4 *>(o) = w;
-        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
+        for (int i = 0; i < kPieces; ++i)
+            w[i] = uint4{u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
+    }
+    __device__ __forceinline__ void values(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (FP32) f[4 * i + j] = __uint_as_float(u[j]);
+                else f[2 * j] = bf16_lo(u[j]), f[2 * j + 1] = bf16_hi(u[j]);
+            }
         }
     }
-}
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (FP32)
+                w[i] = __builtin_bit_cast(uint4, float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]});
+            else
+                w[i] = uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                             pack_bf16(f[6], f[7])};
+        }
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t at) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) bstore16(r, (int)(at + 16 * i), w[i]);
+    }
+    __device__ __forceinline__ void store_some(void *row, int at, bool on) const {
+        if (!on) return;
+        uint8_t *p = reinterpret_cast<uint8_t *>(row) + at;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint4 q = w[j * kSize / 16];
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+            if constexpr (FP32) reinterpret_cast<uint32_t *>(p)[j] = u[j % 4];
+            else reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(u[j / 2 % 4] >> (j % 2 * 16));
+        }
+    }
+};
+
+// The heads of one token, rows of [heads][D]: piece i holds heads i kHeads, ...
+template <bool FP32, int V, int LPV>
+struct Heads {
+    const uint8_t *row;
+    __amdgpu_buffer_rsrc_t r;
+    int heads;
+
+    static constexpr int kHeads = kWave / LPV;
+    __device__ __forceinline__ Heads(const void *x, int64_t at, int heads, int D)
+        : row(reinterpret_cast<const uint8_t *>(x) + at * Raw<FP32, V>::kSize),
+          r(make_rsrc(row, (int64_t)heads * D * Raw<FP32, V>::kSize)), heads(heads) {}
+    static __device__ __forceinline__ int pieces(int heads) { return (heads + kHeads - 1) / kHeads; }
+};
 
 // LPV lanes a head, V values a lane; `parts` waves a token.
-template <bool FP32, int V, int LPV>
-__global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts, bool vec) {
+template <bool FP32, bool VEC, int V, int LPV>
+__global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts) {
+    using Row = Heads<FP32, V, LPV>;
+    using Values = Raw<FP32, V>;
     __shared__ RopeLds lds[4];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lane = threadIdx.x % kWave, d = lane % LPV * V, first = lane / LPV * LPV;
     const uint32_t unit = blockIdx.x * 4 + wave;
     const int64_t row = unit / (uint32_t)parts;
     if (row >= a.T) return;
-    const int per = (a.heads + kWave / LPV - 1) / (kWave / LPV);  // pieces of the token
-    const int step = (per + parts - 1) / parts;
+    const int per = Row::pieces(a.heads), step = (per + parts - 1) / parts;
     const int i0 = (int)(unit % (uint32_t)parts) * step, i1 = min(i0 + step, per);
-    const int64_t from = row * a.ldx, to = row * a.ldo;
-    float f[kAhead][V];
+    const Row from(a.x, row * a.ldx, a.heads, a.D), to(a.out, row * a.ldo, a.heads, a.D);
+    const uint32_t at = d < a.D ? (lane / LPV * a.D + d) * Values::kSize : kOOB;
+    const uint32_t next = Row::kHeads * a.D * Values::kSize;
+    auto on = [&](int i) { return d < a.D && i * Row::kHeads + lane / LPV < a.heads; };
+    Values x[kAhead];
     auto load = [&](int i) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int h = (i + u) * (kWave / LPV) + lane / LPV;
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[u][j] = 0.0f;
-            if (i + u < i1 && h < a.heads && d < a.D)
-                load_values<FP32>(a.x, from + h * a.D + d, vec, f[u]);
+            if (i + u >= i1) break;
+            if constexpr (VEC) x[u].load(from.r, at + (i + u) * next);
+            else x[u].load_some(from.row, (int)(at + (i + u) * next), on(i + u));
         }
     };
     load(i0);  // (in flight while the angles are computed)
@@ -190,9 +217,13 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts, bool vec) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (i + u >= i1) break;
-            const int h = (i + u) * (kWave / LPV) + lane / LPV;
-            rotate<V>(a.rope, t, first, lds[wave].swap, f[u]);
-            if (h < a.heads && d < a.D) store_values<FP32>(a.out, to + h * a.D + d, vec, f[u]);
+            float f[V];
+            x[u].values(f);
+            rotate<V>(a.rope, t, first, lds[wave].swap, f);
+            Values y;
+            y.set(f);
+            if constexpr (VEC) y.store(to.r, at + (i + u) * next);
+            else y.store_some(const_cast<uint8_t *>(to.row), (int)(at + (i + u) * next), on(i + u));
         }
     }
 }
@@ -264,41 +295,37 @@ __device__ __forceinline__ void cache_values(const KvView &c, bool isv, int64_t 
 
 // The pieces of a token are those of its queries, then of its keys, then of its
 // values, each kind a whole number of pieces.
-template <bool INT8, bool FP32, int V, int LPV>
-__global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int parts, bool vecq,
-                                                        bool veckv) {
+template <bool INT8, bool FP32, bool VEC, int V, int LPV>
+__global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int parts) {
+    using Row = Heads<FP32, V, LPV>;
+    using Values = Raw<FP32, V>;
     __shared__ RopeLds lds[4];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lane = threadIdx.x % kWave, d = lane % LPV * V, first = lane / LPV * LPV;
     const uint32_t unit = blockIdx.x * 4 + wave;
     const int64_t row = unit / (uint32_t)parts;
     if (row >= a.rows.T) return;
-    constexpr int kHeads = kWave / LPV;
     const int D = a.c.D, heads = a.c.heads;
-    const int nq = (a.hq + kHeads - 1) / kHeads, nk = (heads + kHeads - 1) / kHeads;
+    const int nq = Row::pieces(a.hq), nk = Row::pieces(heads);
     const int per = nq + 2 * nk, step = (per + parts - 1) / parts;
     const int i0 = (int)(unit % (uint32_t)parts) * step, i1 = min(i0 + step, per);
-    struct Piece {
-        const void *src;
-        int64_t at;
-        int kind, head, heads;  // 0: q, 1: k, 2: v
-        bool vec;
-    };
-    auto piece = [&](int i) {
-        if (i < nq) return Piece{a.q, row * a.ldq, 0, i * kHeads, a.hq, vecq};
-        if (i < nq + nk) return Piece{a.k, row * a.ldk, 1, (i - nq) * kHeads, heads, veckv};
-        return Piece{a.v, row * a.ldv, 2, (i - nq - nk) * kHeads, heads, veckv};
-    };
-    float f[kAhead][V];
+    const Row q(a.q, row * a.ldq, a.hq, D), k(a.k, row * a.ldk, heads, D), v(a.v, row * a.ldv, heads, D);
+    const Row to(a.out, row * a.ldo, a.hq, D);
+    const uint32_t at = d < D ? (lane / LPV * D + d) * Values::kSize : kOOB;
+    const uint32_t next = Row::kHeads * D * Values::kSize;
+    Values x[kAhead];
     auto load = [&](int i) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[u][j] = 0.0f;
-            if (i + u >= i1) continue;
-            const Piece p = piece(i + u);
-            const int h = p.head + lane / LPV;
-            if (h < p.heads && d < D) load_values<FP32>(p.src, p.at + h * D + d, p.vec, f[u]);
+            const int n = i + u;
+            if (n >= i1) break;
+            const int m = n < nq ? n : n < nq + nk ? n - nq : n - nq - nk;
+            if constexpr (VEC) {
+                x[u].load(n < nq ? q.r : n < nq + nk ? k.r : v.r, at + m * next);
+            } else {
+                x[u].load_some(n < nq ? q.row : n < nq + nk ? k.row : v.row, (int)(at + m * next),
+                               d < D && m * Row::kHeads + lane / LPV < (n < nq ? a.hq : heads));
+            }
         }
     };
     load(i0);  // (in flight during the search for the place, and while the angles are computed)
@@ -309,16 +336,22 @@ __global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int pa
         if (i > i0) load(i);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (i + u >= i1) break;
-            const Piece p = piece(i + u);
-            const int h = p.head + lane / LPV;
-            const bool on = h < p.heads && d < D;
-            if (p.kind < 2) rotate<V>(a.rope, t, first, lds[wave].swap, f[u]);
-            if (p.kind == 0) {
-                if (on) store_values<FP32>(a.out, row * a.ldo + h * D + d, vecq, f[u]);
+            const int n = i + u;
+            if (n >= i1) break;
+            float f[V];
+            x[u].values(f);
+            if (n < nq + nk) rotate<V>(a.rope, t, first, lds[wave].swap, f);
+            if (n < nq) {
+                Values y;
+                y.set(f);
+                if constexpr (VEC) y.store(to.r, at + n * next);
+                else y.store_some(const_cast<uint8_t *>(to.row), (int)(at + n * next),
+                                  d < D && n * Row::kHeads + lane / LPV < a.hq);
             } else if (place.at >= 0) {
-                cache_values<INT8, V, LPV>(a.c, p.kind == 2, place.at + ((int64_t)h << a.c.shift), d,
-                                           on, f[u]);
+                const bool isv = n >= nq + nk;
+                const int h = (isv ? n - nq - nk : n - nq) * Row::kHeads + lane / LPV;
+                cache_values<INT8, V, LPV>(a.c, isv, place.at + ((int64_t)h << a.c.shift), d,
+                                           h < heads && d < D, f);
             }
         }
     }
@@ -351,8 +384,9 @@ static void go_rope(const RopeArgs &a, hipStream_t st) {
     by_head<FP32>(a.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value;
         const int parts = parts_of(a.T, (a.heads + kWave / LPV - 1) / (kWave / LPV));
-        launch_kv(k_rope<FP32, V, LPV>, dim3((unsigned)((a.T * parts + 3) / 4)), dim3(256), 0, st, a,
-                  parts, vec);
+        const dim3 g((unsigned)((a.T * parts + 3) / 4));
+        if (vec) launch_kv(k_rope<FP32, true, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else launch_kv(k_rope<FP32, false, V, LPV>, g, dim3(256), 0, st, a, parts);
     });
 }
 
@@ -364,13 +398,14 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t st) {
 
 template <bool INT8, bool FP32>
 static void go_append(const AppendRopeArgs &a, hipStream_t st) {
-    const bool vecq = aligned16(a.q, a.ldq, FP32) && aligned16(a.out, a.ldo, FP32);
-    const bool veckv = aligned16(a.k, a.ldk, FP32) && aligned16(a.v, a.ldv, FP32);
+    const bool vec = aligned16(a.q, a.ldq, FP32) && aligned16(a.out, a.ldo, FP32) &&
+                     aligned16(a.k, a.ldk, FP32) && aligned16(a.v, a.ldv, FP32);
     by_head<FP32>(a.c.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value, H = kWave / LPV;
         const int parts = parts_of(a.rows.T, (a.hq + H - 1) / H + 2 * ((a.c.heads + H - 1) / H));
-        launch_kv(k_kv_append_rope<INT8, FP32, V, LPV>, dim3((unsigned)((a.rows.T * parts + 3) / 4)),
-                  dim3(256), 0, st, a, parts, vecq, veckv);
+        const dim3 g((unsigned)((a.rows.T * parts + 3) / 4));
+        if (vec) launch_kv(k_kv_append_rope<INT8, FP32, true, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else launch_kv(k_kv_append_rope<INT8, FP32, false, V, LPV>, g, dim3(256), 0, st, a, parts);
     });
 }
 

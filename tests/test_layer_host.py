@@ -71,7 +71,7 @@ def rope(s="spec", **kw):
 @pytest.mark.parametrize("kw,rc", [
     (dict(x=None), NULL), (dict(pos=None), NULL), (dict(out=None), NULL), (dict(xt=2), ARG),
     (dict(T=0), SHAPE), (dict(T=(1 << 23) + 1), SHAPE), (dict(heads=0), SHAPE),
-    (dict(heads=1 << 25), SHAPE), (dict(heads=1 << 60), SHAPE), (dict(D=63), SHAPE),
+    (dict(heads=1 << 25), SHAPE), (dict(heads=65536, T=1, ldx=1 << 23, ldo=1 << 23), SHAPE), (dict(heads=1 << 60), SHAPE), (dict(D=63), SHAPE),
     (dict(D=65), SHAPE), (dict(D=520, ldx=4096, ldo=4096), SHAPE), (dict(D=32), SHAPE),
     (dict(ldx=127, ldo=127), SHAPE), (dict(ldo=127), SHAPE), (dict(ldo=1 << 46), SHAPE),
     (dict(ldo=256), ARG),  # in place with another stride
