@@ -106,6 +106,14 @@ __device__ __forceinline__ void rotate(const RopeView &r, const Turn<V> &t, int 
     }
 }
 
+// How rows are read: a value at a time where an address or a stride is aligned to
+// elements only; through the caches where heads end inside a line of 128 bytes, which
+// two loads then share; else past them.  (us, past / through: 8191 tokens of 40 heads
+// of 128 fp32, output in memory that the last call's had, 51 / 63; in new memory 65 /
+// 66; heads of 80 bf16 32 / 29.  The output goes through the caches for the attention
+// that reads it, past them 63 in either.)
+enum { kSome, kCached, kStream };
+
 // V values of a lane as they lie in memory, so that a load waits for nothing.
 template <bool FP32, int V>
 struct Raw {
@@ -113,9 +121,11 @@ struct Raw {
     uint4 w[kPieces];
 
     // beyond the row's range: zeros
+    template <int MODE>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) w[i] = bload16_nt(r, (int)(at + 16 * i));
+        for (int i = 0; i < kPieces; ++i)
+            w[i] = MODE == kStream ? bload16_nt(r, (int)(at + 16 * i)) : bload16(r, (int)(at + 16 * i));
     }
     // the same for rows that are aligned to their elements only
     __device__ __forceinline__ void load_some(const void *row, int at, bool on) {
@@ -185,7 +195,7 @@ struct Heads {
 };
 
 // LPV lanes a head, V values a lane; `parts` waves a token.
-template <bool FP32, bool VEC, int V, int LPV>
+template <bool FP32, int MODE, int V, int LPV>
 __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts) {
     using Row = Heads<FP32, V, LPV>;
     using Values = Raw<FP32, V>;
@@ -206,7 +216,7 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (i + u >= i1) break;
-            if constexpr (VEC) x[u].load(from.r, at + (i + u) * next);
+            if constexpr (MODE != kSome) x[u].template load<MODE>(from.r, at + (i + u) * next);
             else x[u].load_some(from.row, (int)(at + (i + u) * next), on(i + u));
         }
     };
@@ -222,7 +232,7 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int parts) {
             rotate<V>(a.rope, t, first, lds[wave].swap, f);
             Values y;
             y.set(f);
-            if constexpr (VEC) y.store(to.r, at + (i + u) * next);
+            if constexpr (MODE != kSome) y.store(to.r, at + (i + u) * next);
             else y.store_some(const_cast<uint8_t *>(to.row), (int)(at + (i + u) * next), on(i + u));
         }
     }
@@ -295,7 +305,7 @@ __device__ __forceinline__ void cache_values(const KvView &c, bool isv, int64_t 
 
 // The pieces of a token are those of its queries, then of its keys, then of its
 // values, each kind a whole number of pieces.
-template <bool INT8, bool FP32, bool VEC, int V, int LPV>
+template <bool INT8, bool FP32, int MODE, int V, int LPV>
 __global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int parts) {
     using Row = Heads<FP32, V, LPV>;
     using Values = Raw<FP32, V>;
@@ -320,8 +330,8 @@ __global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int pa
             const int n = i + u;
             if (n >= i1) break;
             const int m = n < nq ? n : n < nq + nk ? n - nq : n - nq - nk;
-            if constexpr (VEC) {
-                x[u].load(n < nq ? q.r : n < nq + nk ? k.r : v.r, at + m * next);
+            if constexpr (MODE != kSome) {
+                x[u].template load<MODE>(n < nq ? q.r : n < nq + nk ? k.r : v.r, at + m * next);
             } else {
                 x[u].load_some(n < nq ? q.row : n < nq + nk ? k.row : v.row, (int)(at + m * next),
                                d < D && m * Row::kHeads + lane / LPV < (n < nq ? a.hq : heads));
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int pa
             if (n < nq) {
                 Values y;
                 y.set(f);
-                if constexpr (VEC) y.store(to.r, at + n * next);
+                if constexpr (MODE != kSome) y.store(to.r, at + n * next);
                 else y.store_some(const_cast<uint8_t *>(to.row), (int)(at + n * next),
                                   d < D && n * Row::kHeads + lane / LPV < a.hq);
             } else if (place.at >= 0) {
@@ -381,12 +391,14 @@ static void by_head(int D, F f) {
 template <bool FP32>
 static void go_rope(const RopeArgs &a, hipStream_t st) {
     const bool vec = aligned16(a.x, a.ldx, FP32) && aligned16(a.out, a.ldo, FP32);
+    const bool lines = a.D * (FP32 ? 4 : 2) % 128 == 0;
     by_head<FP32>(a.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value;
         const int parts = parts_of(a.T, (a.heads + kWave / LPV - 1) / (kWave / LPV));
         const dim3 g((unsigned)((a.T * parts + 3) / 4));
-        if (vec) launch_kv(k_rope<FP32, true, V, LPV>, g, dim3(256), 0, st, a, parts);
-        else launch_kv(k_rope<FP32, false, V, LPV>, g, dim3(256), 0, st, a, parts);
+        if (!vec) launch_kv(k_rope<FP32, kSome, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else if (!lines) launch_kv(k_rope<FP32, kCached, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else launch_kv(k_rope<FP32, kStream, V, LPV>, g, dim3(256), 0, st, a, parts);
     });
 }
 
@@ -400,12 +412,14 @@ template <bool INT8, bool FP32>
 static void go_append(const AppendRopeArgs &a, hipStream_t st) {
     const bool vec = aligned16(a.q, a.ldq, FP32) && aligned16(a.out, a.ldo, FP32) &&
                      aligned16(a.k, a.ldk, FP32) && aligned16(a.v, a.ldv, FP32);
+    const bool lines = a.c.D * (FP32 ? 4 : 2) % 128 == 0;
     by_head<FP32>(a.c.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value, H = kWave / LPV;
         const int parts = parts_of(a.rows.T, (a.hq + H - 1) / H + 2 * ((a.c.heads + H - 1) / H));
         const dim3 g((unsigned)((a.rows.T * parts + 3) / 4));
-        if (vec) launch_kv(k_kv_append_rope<INT8, FP32, true, V, LPV>, g, dim3(256), 0, st, a, parts);
-        else launch_kv(k_kv_append_rope<INT8, FP32, false, V, LPV>, g, dim3(256), 0, st, a, parts);
+        if (!vec) launch_kv(k_kv_append_rope<INT8, FP32, kSome, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else if (!lines) launch_kv(k_kv_append_rope<INT8, FP32, kCached, V, LPV>, g, dim3(256), 0, st, a, parts);
+        else launch_kv(k_kv_append_rope<INT8, FP32, kStream, V, LPV>, g, dim3(256), 0, st, a, parts);
     });
 }
 
