@@ -75,12 +75,28 @@ __device__ __forceinline__ void cut3(const float (&f)[8], v8bf (&out)[3]) {
     }
 }
 
-// Eight bf16 from p, the first `n` of them valid, zeros for the others.
+// Eight bf16 from p (aligned to 2 bytes), the first `n` of them valid, zeros for
+// the others: whole pieces while there are some, the rest one by one.
 __device__ __forceinline__ uint4 some8(const uint16_t *p, int n) {
-    uint32_t w[8];
+    uint4 v{};
+    if (n >= 8) {
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    }
+    uint32_t w[8] = {};
+    int j = 0;
+    if (n >= 4) {
+        uint2 u;
+        __builtin_memcpy(&u, p, 8);
+        v.x = u.x, v.y = u.y;
+        j = 4;
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0u;
-    return uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+    for (int e = 0; e < 3; ++e) w[e] = j + e < n ? p[j + e] : 0u;
+    const uint32_t lo = w[0] | w[1] << 16, hi = w[2];
+    if (n >= 4) v.z = lo, v.w = hi;
+    else v.x = lo, v.y = hi;
+    return v;
 }
 
 // Which of eight bf16 to keep, the first `n` (the others may hold anything).
@@ -98,6 +114,11 @@ template <bool FP32> struct Chunk;
 template <> struct Chunk<true> {
     float4 a, b;
     __device__ __forceinline__ void some(const float *p, int n) {
+        if (n >= 8) {
+            __builtin_memcpy(&a, p, 16);
+            __builtin_memcpy(&b, p + 4, 16);
+            return;
+        }
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = j < n ? p[j] : 0.0f;
@@ -366,27 +387,29 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
                                          ch + c16 < len ? rank - 32 * s - 8 * q : 0);
                 }
         };
+        // this lane's channels: 4 lane + e, or lane + 64 e where Y goes value by value
+        auto channel = [&](int e) { return YVEC ? 4 * lane + e : lane + 64 * e; };
         auto each_y = [&](int n, auto f) {
-            const int left = len - (n + 4 * lane);
 #pragma unroll
             for (int i = 0; i < 4 * MT; ++i) {
                 const int m = wave + 4 * i;
                 if (!(match >> m & 1)) continue;
-                float *at = rows + m * a.ldy + n + 4 * lane;
+                float *at = rows + m * a.ldy + n;
                 if constexpr (YVEC) {
-                    if (left > 0) f(i, m, [&](v4f &v) { v = *reinterpret_cast<const v4f *>(at); },
-                                    [&](const v4f &v) { *reinterpret_cast<v4f *>(at) = v; });
+                    if (n + 4 * lane < len)
+                        f(i, m, [&](v4f &v) { v = *reinterpret_cast<const v4f *>(at + 4 * lane); },
+                          [&](const v4f &v) { *reinterpret_cast<v4f *>(at + 4 * lane) = v; });
                 } else {
                     f(i, m,
                       [&](v4f &v) {
 #pragma unroll
                           for (int e = 0; e < 4; ++e)
-                              if (e < left) v[e] = at[e];
+                              if (n + channel(e) < len) v[e] = at[channel(e)];
                       },
                       [&](const v4f &v) {
 #pragma unroll
                           for (int e = 0; e < 4; ++e)
-                              if (e < left) at[e] = v[e];
+                              if (n + channel(e) < len) at[channel(e)] = v[e];
                       });
                 }
             }
@@ -448,10 +471,9 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
             if (next < len) load_b(next);
             lds_barrier();
             each_y(n, [&](int i, int m, auto, auto put) {
-                const v4f d = *reinterpret_cast<const v4f *>(&D[m][4 * lane]);
                 v4f v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(scale, d[e], y[i][e]);
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(scale, D[m][channel(e)], y[i][e]);
                 put(v);
             });
             if (next >= len) break;

@@ -179,17 +179,20 @@ __device__ __forceinline__ void store_piece(void *p, int64_t at, const float (&f
     }
 }
 
+// Rows of one wave (T = 64) share a workgroup of four and no barrier.
 template <bool FP32, int OUT, bool RES, int V, int T, int NG>
-__global__ __launch_bounds__(T) void k_rms_norm(NormArgs a) {
-    constexpr int kWaves = T / kWave;
+__global__ __launch_bounds__(T > 256 ? T : 256) void k_rms_norm(NormArgs a) {
+    constexpr int kWaves = T / kWave, kRows = T > kWave ? 1 : 4;
     __shared__ double red[kWaves];
     __shared__ uint32_t redm[kWaves];
-    const int64_t m = blockIdx.x, K = a.K;
+    const int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / T, K = a.K;
+    const int tid = threadIdx.x % T;
+    if (kRows > 1 && m >= a.M) return;
     const int ng = (int)K / V;
     float h[NG][V], r[NG][V], w[NG][V];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-        const int g = threadIdx.x + T * u;
+        const int g = tid + T * u;
 #pragma unroll
         for (int j = 0; j < V; ++j) h[u][j] = 0.0f, r[u][j] = 0.0f, w[u][j] = 1.0f;
         if (g >= ng) continue;
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(T) void k_rms_norm(NormArgs a) {
     double ss = 0.0;
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-        const int g = threadIdx.x + T * u;
+        const int g = tid + T * u;
         if constexpr (RES) {
 #pragma unroll
             for (int j = 0; j < V; ++j) h[u][j] += r[u][j];
@@ -230,13 +233,13 @@ __global__ __launch_bounds__(T) void k_rms_norm(NormArgs a) {
         for (int u = 0; u < NG; ++u)
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (threadIdx.x + T * u < ng) top = max(top, abs_bits(h[u][j]));
+                if (tid + T * u < ng) top = max(top, abs_bits(h[u][j]));
         const float sx = row_scale_of<kWaves>(top, redm);
-        if (threadIdx.x == 0) a.sx[m] = sx;
+        if (tid == 0) a.sx[m] = sx;
         auto codes = [&](auto code) {
 #pragma unroll
             for (int u = 0; u < NG; ++u) {
-                const int g = threadIdx.x + T * u;
+                const int g = tid + T * u;
                 if (g >= ng) continue;
                 int8_t *o = reinterpret_cast<int8_t *>(a.out) + m * K + V * g;
                 const float(&f)[V] = h[u];
@@ -263,7 +266,7 @@ __global__ __launch_bounds__(T) void k_rms_norm(NormArgs a) {
     } else {
 #pragma unroll
         for (int u = 0; u < NG; ++u) {
-            const int g = threadIdx.x + T * u;
+            const int g = tid + T * u;
             if (g < ng) store_piece<OUT == RMS_FP32, true>(a.out, m * K + V * g, h[u]);
         }
     }
@@ -276,28 +279,31 @@ static void launch_as(const NormArgs &a, const char **path, hipStream_t st) {
     const bool whole = a.K % V == 0 && a.ldx % V == 0 && at(a.x, 16) && at(a.res, 16) &&
                        at(a.sum, 16) && at(a.weight, 16) &&
                        at(a.out, OUT == kNormInt8 ? V : OUT == RMS_FP32 ? 16 : 2 * V);
-    const dim3 g((unsigned)a.M);
     auto go = [&](auto v, auto t, auto values) {
         constexpr int P = decltype(v)::value, T = decltype(t)::value;
         constexpr int NG = decltype(values)::value / P;
+        const dim3 g((unsigned)(T > kWave ? a.M : (a.M + 3) / 4)), b(T > kWave ? T : 256);
         *path = P > 1 ? "rms_norm" : "rms_norm_odd";
-        if (a.res) launch_kv(k_rms_norm<FP32, OUT, true, P, T, NG>, g, dim3(T), 0, st, a);
-        else launch_kv(k_rms_norm<FP32, OUT, false, P, T, NG>, g, dim3(T), 0, st, a);
+        if (a.res) launch_kv(k_rms_norm<FP32, OUT, true, P, T, NG>, g, b, 0, st, a);
+        else launch_kv(k_rms_norm<FP32, OUT, false, P, T, NG>, g, b, 0, st, a);
     };
     auto run = [&](auto t, auto values) { go(Int<V>{}, t, values); };
     // Up to 32 values a thread, and the fewest threads that this allows: they meet at
     // fewer barriers (8192 rows of 8192, us: 256 / 512 / 1024 threads 151 / 156 / 153;
     // 64 rows of 4096: 3.6 / 3.6 / 5.2).
+    if (whole && a.K <= 512) return run(Int<64>{}, Int<8>{});
     if (whole && a.K <= 2048) return run(Int<256>{}, Int<8>{});
     if (whole && a.K <= 4096) return run(Int<256>{}, Int<16>{});
     if (whole && a.K <= 8192) return run(Int<256>{}, Int<32>{});
     if (whole && a.K <= 16384) return run(Int<512>{}, Int<32>{});
     if (whole && a.K <= 32768) return run(Int<1024>{}, Int<32>{});
+    if (!whole && a.K <= 512) return go(Int<1>{}, Int<64>{}, Int<8>{});
+    if (!whole && a.K <= 2048) return go(Int<1>{}, Int<256>{}, Int<8>{});
     if (!whole && a.K <= 8192) return go(Int<1>{}, Int<256>{}, Int<32>{});
     if (!whole && a.K <= 16384) return go(Int<1>{}, Int<512>{}, Int<32>{});
     if (!whole && a.K <= 32768) return go(Int<1>{}, Int<1024>{}, Int<32>{});
     *path = "rms_norm_long";
-    launch_kv(k_rms_norm_long<FP32, OUT>, g, dim3(1024), 0, st, a);
+    launch_kv(k_rms_norm_long<FP32, OUT>, dim3((unsigned)a.M), dim3(1024), 0, st, a);
 }
 
 hipError_t launch_rms_norm(const NormArgs &a, const char **path, hipStream_t st) {

@@ -199,3 +199,16 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         want = w4.a8_rms_norm(xc, wc, 1e-5, residual=rc)
         assert all(torch.equal(a, b) for a, b in zip(want, (q, sx, s)))
+
+
+@pytest.mark.parametrize("M,K", [(4097, 90), (1001, 128), (513, 512), (6, 3), (10, 513), (2049, 16)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_many_short_rows(M, K, dt):
+    x, r, w = make(M, K, dt, True, M)
+    y, h = formula(x, r, w, 0.0, 1e-6)
+    xc, rc, wc = cuda(x, r, w)
+    o, s = w4.rms_norm(xc, wc, 1e-6, residual=rc, dtype=torch.float32)
+    assert torch.equal(o.cpu(), y) and torch.equal(s.cpu(), h.to(dt))
+    q, sx, _ = w4.a8_rms_norm(xc, wc, 1e-6, residual=rc)
+    q2, sx2 = w4.a8_quantize_act(o)
+    assert torch.equal(q, q2) and torch.equal(sx, sx2)
