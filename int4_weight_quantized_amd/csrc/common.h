@@ -179,6 +179,13 @@ __device__ __forceinline__ void dma16(v4i rsrc, uint32_t lds_base, int voff, int
                  : "memory");
 }
 
+// The same past the caches (non-temporal): for data that a kernel reads once.
+__device__ __forceinline__ void dma16_nt(v4i rsrc, uint32_t lds_base, int voff, int soff) {
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 ::"v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_base)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void *)p));
 }
