@@ -4,7 +4,9 @@ forked samples, entirely on the device.
 Quantized projections (W4A8) around the cache: prompts are written and attended
 in one call each, two of them are forked into more samples, every step reserves
 a page where one is due, writes one token for each running slot and attends it,
-a sample is retired, and the pool is made dense.
+a sample is retired, and the pool is made dense.  Optionally the block has a norm
+in front of its first projection, rotary positions, and an adapter for each
+request beside that projection's shared weight.
 
     python examples/decode_layer.py
 """
@@ -20,11 +22,15 @@ import int4_weight_quantized_amd as w4  # noqa: E402
 
 
 class Block:
-    """x -> x + Wo attention(Wqkv x): W4A8 projections, a paged cache of `layers` layers."""
+    """x -> x + Wo attention(Wqkv x): W4A8 projections, a paged cache of `layers` layers.
+
+    norm: an RMS norm of x in front of Wqkv; rope: rotary positions of queries and keys;
+    adapters: as many low-rank adapters of Wqkv, self.adapter naming each slot's (-1: none)."""
 
     def __init__(self, hidden: int, q_heads: int, kv_heads: int, head_dim: int, slots: int,
                  pages: int, pages_per_slot: int, page_size: int = 16, dtype=torch.int8,
-                 layers: int = 1, seed: int = 0):
+                 layers: int = 1, seed: int = 0, norm: bool = False, rope: w4.Rope = None,
+                 adapters: int = 0, rank: int = 16):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.hq, self.h, self.d = q_heads, kv_heads, head_dim
         n = (q_heads + 2 * kv_heads) * head_dim
@@ -36,11 +42,36 @@ class Block:
         self.table = torch.full((slots, pages_per_slot), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros((slots,), dtype=torch.int32, device="cuda")
         self.refs = torch.zeros((pages,), dtype=torch.int32, device="cuda")
+        self.norm = 1 + 0.1 * torch.randn((hidden,), generator=g, device="cuda") if norm else None
+        self.rope = rope
+        self.adapter = torch.full((slots,), -1, dtype=torch.int32, device="cuda")
+        if adapters:
+            self.A = (torch.randn((adapters, rank, hidden), generator=g, device="cuda")
+                      * hidden ** -0.5).bfloat16()
+            self.B = (0.1 * torch.randn((adapters, n, rank), generator=g, device="cuda")).bfloat16()
+        self.adapters = adapters
 
-    def project(self, x: torch.Tensor):
-        """(q, k, v) of rows x [T, hidden]: slices of one product's rows."""
-        y = w4.w4a8_linear(x, self.wqkv, self.sqkv).unflatten(1, (-1, self.d))
+    def project(self, x: torch.Tensor, adapter: torch.Tensor = None):
+        """(q, k, v) of rows x [T, hidden]: slices of one product's rows; adapter [T]:
+        each row's."""
+        if self.norm is not None and not self.adapters:
+            xq, sx, _ = w4.a8_rms_norm(x, self.norm, 1e-6)  # int8 rows, as the product takes them
+            y = w4.w4a8_linear_q(xq, sx, self.wqkv, self.sqkv)
+        else:
+            if self.norm is not None:
+                x, _ = w4.rms_norm(x, self.norm, 1e-6)
+            y = w4.w4a8_linear(x, self.wqkv, self.sqkv)
+            if self.adapters:
+                w4.lora_add(y, x, adapter, self.A, self.B)
+        y = y.unflatten(1, (-1, self.d))
         return y[:, :self.hq], y[:, self.hq:self.hq + self.h], y[:, self.hq + self.h:]
+
+    def append(self, layer, q, k, v, table, start, cu=None) -> torch.Tensor:
+        """Tokens into the cache; the queries as the attention takes them."""
+        if self.rope is None:
+            w4.kv_append(self.cache, layer, k, v, table, start, cu)
+            return q
+        return w4.kv_append_rope(self.cache, layer, q, k, v, table, start, self.rope, cu, out=q)
 
     def output(self, x: torch.Tensor, o: torch.Tensor) -> torch.Tensor:
         return x + w4.w4a8_linear(o.flatten(1), self.wo, self.so)
@@ -56,8 +87,10 @@ class Block:
         ok = self.reserve(add)
         self.lens += add * ok
         table, lens = self.table[slots.long()], self.lens[slots.long()]
-        q, k, v = self.project(x)
-        w4.kv_append(self.cache, layer, k, v, table, torch.zeros_like(lens), cu)
+        rows = torch.repeat_interleave(self.adapter[slots.long()], cu[1:] - cu[:-1],
+                                       output_size=x.shape[0]) if self.adapters else None
+        q, k, v = self.project(x, rows)
+        q = self.append(layer, q, k, v, table, torch.zeros_like(lens), cu)
         o = w4.kv_prefill_attention(q, self.cache, layer, table, lens, cu, window=window, sinks=sinks)
         return self.output(x, o), q, o
 
@@ -66,14 +99,15 @@ class Block:
         running = (self.lens > 0).to(torch.int32)
         running *= self.reserve(running)
         start = torch.where(running > 0, self.lens, -1)  # -1: takes no token
-        q, k, v = self.project(x)
-        w4.kv_append(self.cache, layer, k, v, self.table, start)
+        q, k, v = self.project(x, self.adapter)
+        q = self.append(layer, q, k, v, self.table, start)
         self.lens += running
         o = w4.kv_decode_attention(q, self.cache, layer, self.table, self.lens * running,
                                    window=window, sinks=sinks)
         return self.output(x, o), q, o
 
     def fork(self, parents, children) -> torch.Tensor:
+        self.adapter[children.long()] = self.adapter[parents.long()]
         return w4.kv_fork(self.cache, self.table, self.lens, self.refs, parents, children)
 
     def free(self, slots) -> None:
@@ -88,10 +122,13 @@ def ints(*v) -> torch.Tensor:
 
 
 def serve(steps: int = 20, hidden: int = 1152, dtype=torch.int8, window: int = 0, sinks: int = 0,
-          seen=lambda block, what, q, o: None) -> Block:
-    """Two prompts, five samples, `steps` tokens each; `seen` looks at each call."""
+          seen=lambda block, what, q, o: None, **kw) -> Block:
+    """Two prompts, five samples, `steps` tokens each; `seen` looks at each call;
+    kw: the block's norm, rope and adapters (the first prompt has the last adapter)."""
     b = Block(hidden, q_heads=8, kv_heads=2, head_dim=128, slots=8, pages=96, pages_per_slot=24,
-              dtype=dtype)
+              dtype=dtype, **kw)
+    if b.adapters:
+        b.adapter[5] = b.adapters - 1
     g = torch.Generator(device="cuda").manual_seed(1)
     cu = ints(0, 37, 237)
     x = torch.randn((237, hidden), generator=g, device="cuda")
@@ -109,7 +146,7 @@ def serve(steps: int = 20, hidden: int = 1152, dtype=torch.int8, window: int = 0
 
 
 if __name__ == "__main__":
-    block = serve()
+    block = serve(norm=True, rope=w4.Rope(128), adapters=3)
     print("lengths", block.lens.tolist())
     print("pages held", int((block.refs > 0).sum()), "of", block.refs.numel(),
           "- shared", int((block.refs > 1).sum()))
