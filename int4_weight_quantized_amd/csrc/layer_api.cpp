@@ -40,6 +40,7 @@ int norm(const void *x, int x_dtype, int64_t ldx, const void *res, const float *
         return W4_ERR_ARG;
     if (M < 1 || K < 1 || M > kMaxRows || K > W4_MAX_K || M > kMaxNorm / K || !rows_ok(M, K, ldx))
         return W4_ERR_SHAPE;
+    if (sum == x && ldx != K) return W4_ERR_ARG;  // the sum's rows lie side by side
     const size_t e = x_size(x_dtype);
     const size_t o = out_type == w4::kNormInt8 ? 1 : out_type == RMS_FP32 ? 4 : 2;
     if (!aligned(x, e) || !aligned(res, e) || !aligned(sum, e) || !aligned(weight, 4) ||

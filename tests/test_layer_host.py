@@ -35,6 +35,7 @@ def norm8(**kw):
     (dict(x=None), NULL), (dict(sum=None), NULL), (dict(res=None), NULL),
     (dict(xt=2), ARG), (dict(xt=-1), ARG), (dict(eps=-1e-9), ARG), (dict(eps=NAN), ARG),
     (dict(eps=INF), ARG), (dict(offset=NAN), ARG), (dict(offset=-INF), ARG),
+    (dict(sum=FAKE, ldx=72), ARG),
     (dict(M=0), SHAPE), (dict(K=0), SHAPE), (dict(M=-1), SHAPE), (dict(ldx=63), SHAPE),
     (dict(M=(1 << 23) + 1), SHAPE), (dict(K=w4.W4_MAX_K + 1, ldx=1 << 18), SHAPE),
     (dict(ldx=1 << 46), SHAPE), (dict(ldx=-64), SHAPE), (dict(M=1 << 22, K=16385, ldx=16385), SHAPE),
