@@ -159,7 +159,8 @@ __device__ __forceinline__ void write_sums(const LoraArgs &a, const LoraPlan &p,
 // Workgroup (tile and slot, part of K, 16 RC rows of A): its four waves take a
 // quarter of the part each and add their sums in LDS.  A is the first operand
 // and X the second, so that a lane ends with four neighbouring values of a row
-// of S.  X is read once (for every 16 RC ranks), straight into registers.
+// of S.  X is read once (for every 16 RC ranks), straight into registers: this form
+// takes every size and alignment (409 rows 451 -> 6342, rank 29: 8 us).
 template <bool FP32, int MT, int RC>
 __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
     constexpr int U = FP32 ? 4 / MT : MT * RC >= 8 ? 1 : 8 / (MT * RC);  // k-steps in flight
@@ -231,9 +232,11 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
 // The same for aligned operands: stages of 128 k go through LDS by direct loads,
 // whole row pieces of 256 and 512 bytes side by side, since the operands' own layout
 // (neighbouring lanes, different rows) costs the address unit four times the cycles
-// (8192 rows, K 4096: 45 us straight into registers, 134 MB).  16-byte pieces of a row are
+// (8192 rows, K 4096, rank 32, 134 MB: 35 us, 45 straight into registers).  X goes past
+// the caches, whose place A has (35 us, 38 through them).  16-byte pieces of a row are
 // stored at their index xor the row, so that 16 rows' reads of one piece hit all
-// banks.  Wave w takes k-step w of each stage; three stages, two of them in flight.
+// banks.  Wave w takes k-step w of each stage; three stages, two of them in flight
+// (two slots 34 us, four 48, for want of a second workgroup).
 template <bool FP32, int MT, int RC>
 __global__ __launch_bounds__(256) void k_lora_down_lds(LoraArgs a, LoraPlan p) {
     constexpr int kTerms = FP32 ? 3 : 1;
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
 constexpr int kMaxSplits = 16;
 constexpr int64_t kSplitRows = 32768;  // rows of S in the workspace beyond the first part, at most
 
-// a tile's 32 rows lie within a descriptor's range
+// A tile's 32 rows lie within a descriptor's range.
 constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 static int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -536,13 +539,17 @@ template <int MT>
 static void go(const LoraArgs &a, hipStream_t st) {
     auto at16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     const int64_t tiles = (a.M + 16 * MT - 1) / (16 * MT);
-    // workgroups of a tile: as many as its adapters can use, or 2048 of the call
+    // Workgroups of a tile: as many as its adapters can use, or 2048 of the call.  Their
+    // index is the slowest: beside the tile's, the idle ones of prompts (one adapter a
+    // tile) left half of the XCDs without work (first launch of 8192 rows 53 us, 45).
     auto slots = [&](int64_t others) {
         const int64_t most = std::min<int64_t>(16 * MT, a.adapters);
         return (int)std::max<int64_t>(1, std::min<int64_t>(most, 2048 / std::max<int64_t>(1, others)));
     };
     LoraPlan p{};
     p.rp = (int)round16(a.rank);
+    // Parts of K of 512 or more (64 rows, K 4096, us for 2 / 4 / 8 / 16 parts: 9.1 / 6.4 / 5.4 /
+    // 6.1), fewer where the tiles fill the GPU (8192 rows, both launches, 2 / 4 / 8: 92 / 85 / 87).
     int64_t splits = std::min<int64_t>(1 + std::min<int64_t>(kMaxSplits - 1, kSplitRows / a.M),
                                        std::min<int64_t>((a.K + 511) / 512, (1024 + tiles - 1) / tiles));
     p.kc = (int)(((a.K + splits - 1) / splits + 127) / 128 * 128);
@@ -555,6 +562,10 @@ static void go(const LoraArgs &a, hipStream_t st) {
 
     const bool bv = a.rank % 8 == 0 && at16(a.B);
     const bool yv = a.N % 4 == 0 && a.ldy % 4 == 0 && at16(a.Y);
+    // Channels of a workgroup: 256, and more where there are workgroups enough, since each
+    // sums S and splits it once (us for 256 / 512 / 1024 / 2048: 64 rows -> 11008, rank 16, 13.8 /
+    // 10.7 / 8.6 / 10.0; 16 rows -> 28672, rank 64, 24 / 18 / 13.5 / 13.8; 8192 rows -> 4096, both
+    // launches, 90 / 85 / 92; one row -> 6912 3.5 / 3.8 / 4.7).
     const int64_t chunks = (a.N + 255) / 256;
     const int64_t per = std::max<int64_t>(1, std::min<int64_t>(
         MT == 1 ? 4 : 2, tiles * std::min<int64_t>(16 * MT, a.adapters) * chunks / 448));
@@ -566,6 +577,9 @@ static void go(const LoraArgs &a, hipStream_t st) {
 
 hipError_t launch_lora(const LoraArgs &a, const char **path, hipStream_t st) {
     *path = "lora";
+    // Tiles of 32 rows halve the traffic of A and B, of 16 spread a step's adapters over
+    // more workgroups (8192 rows, first launch, 32 / 16: 33 / 37 us); more than 128 ranks
+    // of 32 rows would not fit the registers.
     if (a.M <= 256 || a.rank > 128) go<1>(a, st);
     else go<2>(a, st);
     return hipGetLastError();

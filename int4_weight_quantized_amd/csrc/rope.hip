@@ -10,7 +10,8 @@
 // A wave takes one token: it computes the token's angles (64 at once), keeps those
 // of its lanes' values in registers, and goes through the token's heads, 1 KB at a
 // time, four loads ahead; waves share nothing.  Calls of few tokens split a
-// token's heads over several waves, each with the angles.  Bound by memory.
+// token's heads over several waves, each with the angles.  Bound by memory (into the
+// cache: 6984 tokens of 64 / 8 heads of 128, fp32, 543 MB, 86 us, 6.3 TB/s).
 #include <algorithm>
 #include <type_traits>
 
