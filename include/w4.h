@@ -551,7 +551,7 @@ typedef enum { RMS_BF16 = 0, RMS_FP32 = 1 } rms_dtype;
  * zeros with eps 0 is NaN.
  * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
 int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
-             const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+             const float *weight, float offset, double eps, int64_t M, int64_t K, void *sum,
              void *out, int out_dtype, void *stream);
 
 /* The same with int8 rows as w4a8_linear_q takes them: Xq [M][K] and sx [M] are
@@ -561,7 +561,7 @@ int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
  * (For awq_quantize_act of the output, pass fl(offset + weight) / s and offset 0:
  * the division by powers of two is exact.) */
 int a8_rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
-                const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+                const float *weight, float offset, double eps, int64_t M, int64_t K, void *sum,
                 int8_t *Xq, float *sx, void *stream);
 
 /* Rotary positions.  The first rot_dim values of a head are rot_dim / 2 pairs;

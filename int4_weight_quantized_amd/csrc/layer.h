@@ -17,7 +17,8 @@ struct NormArgs {
     bool fp32;            // type of x, res and sum
     int64_t ldx;
     const float *weight;  // NULL: ones
-    float offset, eps;
+    float offset;
+    double eps;
     int64_t M, K;
     void *sum;            // NULL without res
     void *out;            // bf16, fp32 or int8

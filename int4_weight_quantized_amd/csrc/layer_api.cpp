@@ -32,11 +32,11 @@ bool rows_ok(int64_t T, int64_t row, int64_t stride) {
 }
 
 int norm(const void *x, int x_dtype, int64_t ldx, const void *res, const float *weight,
-         float offset, float eps, int64_t M, int64_t K, void *sum, void *out, int out_type,
+         float offset, double eps, int64_t M, int64_t K, void *sum, void *out, int out_type,
          float *sx, void *stream) {
     if (!x || !out || (out_type == w4::kNormInt8 && !sx) || (res != nullptr) != (sum != nullptr))
         return W4_ERR_NULL;
-    if (!x_type(x_dtype) || !std::isfinite(offset) || !std::isfinite(eps) || eps < 0.0f)
+    if (!x_type(x_dtype) || !std::isfinite(offset) || !std::isfinite(eps) || eps < 0.0)
         return W4_ERR_ARG;
     if (M < 1 || K < 1 || M > kMaxRows || K > W4_MAX_K || M > kMaxNorm / K || !rows_ok(M, K, ldx))
         return W4_ERR_SHAPE;
@@ -77,7 +77,7 @@ bool lora_sizes(int64_t M, int64_t K, int64_t N, int64_t rank) {
 extern "C" {
 
 int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
-             const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+             const float *weight, float offset, double eps, int64_t M, int64_t K, void *sum,
              void *out, int out_dtype, void *stream) {
     if (out_dtype != RMS_BF16 && out_dtype != RMS_FP32) return W4_ERR_ARG;
     return norm(x, x_dtype, x_stride, residual, weight, offset, eps, M, K, sum, out, out_dtype,
@@ -85,7 +85,7 @@ int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
 }
 
 int a8_rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
-                const float *weight, float offset, float eps, int64_t M, int64_t K, void *sum,
+                const float *weight, float offset, double eps, int64_t M, int64_t K, void *sum,
                 int8_t *Xq, float *sx, void *stream) {
     return norm(x, x_dtype, x_stride, residual, weight, offset, eps, M, K, sum, Xq,
                 w4::kNormInt8, sx, stream);

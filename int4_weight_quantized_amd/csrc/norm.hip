@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t b) {
 }
 
 template <int kWaves>
-__device__ __forceinline__ float row_rsqrt(double ss, double *red, int64_t K, float eps) {
+__device__ __forceinline__ float row_rsqrt(double ss, double *red, int64_t K, double eps) {
     ss = wave_sum(ss);
     if constexpr (kWaves > 1) {
         if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = ss;
@@ -64,7 +64,7 @@ __device__ __forceinline__ float row_rsqrt(double ss, double *red, int64_t K, fl
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) ss += red[i];
     }
-    return (float)(1.0 / sqrt(ss / (double)K + (double)eps));
+    return (float)(1.0 / sqrt(ss / (double)K + eps));
 }
 
 // The largest |y| of the row as bits, which order as the values do, infinity and

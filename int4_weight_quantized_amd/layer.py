@@ -38,8 +38,8 @@ class _Spec(ctypes.Structure):
 
 
 LAYER_SIGNATURES = {
-    "rms_norm": ([_P, _N, _I, _P, _P, _F, _F, _I, _I, _P, _P, _N, _P], _N),
-    "a8_rms_norm": ([_P, _N, _I, _P, _P, _F, _F, _I, _I, _P, _P, _P, _P], _N),
+    "rms_norm": ([_P, _N, _I, _P, _P, _F, _D, _I, _I, _P, _P, _N, _P], _N),
+    "a8_rms_norm": ([_P, _N, _I, _P, _P, _F, _D, _I, _I, _P, _P, _P, _P], _N),
     "rope_frequencies": ([_I, _D, _N, _D, _I, _D, _D, _P, _P], _N),
     "rope_rotate": ([_P, _P, _N, _I, _I, _I, _I, _P, _P, _I, _P], _N),
     "kv_append_rope": ([_P, _I, _P, _P, _P, _P, _N, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P,

@@ -113,3 +113,44 @@ def test_example_runs():
     b = decode_layer.serve(6, norm=True, rope=w4.Rope(128), adapters=3)
     assert b.lens.tolist() == [43, 43, 206, 0, 0, 0, 0, 0]
     assert b.adapter.tolist()[:2] == [2, 2]
+
+
+@pytest.mark.parametrize("adapters", [0, 3])
+def test_a_captured_step(adapters):
+    """A whole step captured once and replayed, against the same steps one by one."""
+    import decode_layer
+    import int4_weight_quantized_amd as w4
+
+    def block():
+        b = decode_layer.Block(512, 8, 2, 128, slots=4, pages=40, pages_per_slot=10, norm=True,
+                               rope=w4.Rope(128), adapters=adapters)
+        if adapters:
+            b.adapter.copy_(torch.tensor([2, -1, 0, 1], dtype=torch.int32))
+        g = torch.Generator(device="cuda").manual_seed(3)
+        b.prompts(torch.randn((50, 512), generator=g, device="cuda"), decode_layer.ints(3, 0),
+                  decode_layer.ints(0, 30, 50))
+        return b
+
+    one, two = block(), block()
+    x = torch.zeros((4, 512), device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = two.step(x)
+    assert two.lens.tolist() == [20, 0, 0, 30]  # (captured, not run)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for i in range(5):
+        fresh = torch.randn((4, 512), generator=gen, device="cuda")
+        x.copy_(fresh)
+        g.replay()
+        torch.cuda.synchronize()
+        want = one.step(fresh)
+        run = one.lens > 0
+        for a, b in zip(out, want):
+            assert torch.equal(a[run], b[run])
+        assert torch.equal(one.lens, two.lens) and torch.equal(one.table, two.table)
+        cu = decode_layer.ints(0, 20 + i + 1)
+        a, b = (w4.kv_gather(c.cache, 0, c.table[:1].contiguous(), decode_layer.ints(0), cu, 20 + i + 1)
+                for c in (one, two))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert one.lens.tolist() == [25, 0, 0, 35]

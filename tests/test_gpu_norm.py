@@ -55,7 +55,7 @@ def test_norm(M, K, dt, res, offset):
         o, s = w4.rms_norm(xc, wc, 1e-6, residual=rc, offset=offset, dtype=ot)
         assert torch.equal(o.cpu(), y.to(ot))
         assert (s is None) if r is None else torch.equal(s.cpu(), h.to(dt))
-    e = exact(x, r, w, offset, float(torch.tensor(1e-6)))
+    e = exact(x, r, w, offset, 1e-6)
     assert ((y.double() - e).abs() <= 7 * U * e.abs()).all()
     assert ((o.double().cpu() - e).abs() <= (7 * U + 1.01 * U16) * e.abs()).all()
     q, sx, s = w4.a8_rms_norm(xc, wc, 1e-6, residual=rc, offset=offset)
@@ -137,6 +137,9 @@ def test_rows_at_the_ends_of_the_range(K):
     q2, sx2 = w4.a8_quantize_act(o[fine].contiguous())
     assert torch.equal(q[fine], q2) and torch.equal(sx[fine], sx2)
     assert sx[5:8].isnan().all() and sx[1] == 0 and not q[1].any()
+    # eps as it is given, not rounded: rows far below it are scaled by it alone
+    for eps in (1e-6, 1e-5, 3e-7, 1e-12):
+        assert torch.equal(w4.rms_norm(*cuda(x[2:3], w), eps)[0].cpu(), formula(x[2:3], None, w, 0.0, eps)[0])
     # eps 0: a row of zeros is NaN, the others are not touched
     o, _ = w4.rms_norm(*cuda(x[:3], w), 0.0)
     assert o[1].isnan().all() and torch.equal(o.cpu()[::2], formula(x[:3:2], None, w, 0.0, 0.0)[0])

@@ -235,6 +235,23 @@ def test_int8_keys_that_are_not_finite():
     assert a.v_scale[0, page].isnan().sum() == 1 and a.v_scale[0, page, 0, 5].isnan()
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 80, 256])
+def test_int8_scales_of_every_size(D, dt):
+    """Codes and scales of tiny, huge and zero vectors are kv_append's."""
+    sizes = [0.0, 1e-44, 1e-38, 1e-30, 2e-18, 1e-10, 1.0, 1e10, 1e30, 1e38]
+    n = len(sizes)
+    cache, table, start, cu, q, k, v, pos = setting([n], [n], 2, 2, D, 16, "int8", torch.float32, 5)
+    by = torch.tensor(sizes, device="cuda")[:, None, None] / 4
+    q, k, v = ((t * by).to(dt) for t in (q, k, v))
+    v[3, 0] = 0.0
+    rope = w4.Rope(32)
+    a, b = cache(), cache()
+    w4.kv_append_rope(a, 0, q, k, v, table, start, rope, cu)
+    w4.kv_append(b, 0, w4.rope_rotate(k.float(), pos, rope), v.float(), table, start, cu)
+    assert same(a, b)
+
+
 def test_the_far_end_of_a_large_pool():
     """Pages at offsets beyond 32 bits."""
     heads, D, ps = 8, 256, 64
