@@ -14,6 +14,7 @@
 namespace w4 {
 
 template <int N> using Int = std::integral_constant<int, N>;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------ helpers
 __device__ __forceinline__ double dpp_double(double v, int which) {
@@ -129,93 +130,108 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
     }
 }
 
-// Pieces of 16 bytes of x (V = 4 or 8 values), or single values (V = 1) where K, a
-// stride or an address does not allow those: thread t owns pieces t, t + T, ... (NG), all loads issued at once, neighbouring lanes side by
-// side in every array; a row is read once and stays in registers.  x and the
-// residual are read, and the sum written, past the caches, whose place the output
-// has for the product that takes it (8192 rows of 8192, fp32 with residual to bf16,
-// 940 MB: 139 us, 6.8 TB/s; the output past them too 152, all through them 160; one
-// row of 1152 to int8 2.2 us, 64 rows of 4096 with residual 3.8).
+// V values as they lie in memory, 16 bytes (V = 4 or 8) or a single one, so that a
+// load waits for nothing; outside the row's range a load gives zeros and a store
+// writes nothing, which leaves no branch between the loads.
 template <bool FP32, int V>
-__device__ __forceinline__ void load_piece(const void *p, int64_t at, float (&f)[V]) {
+struct Piece {
+    static constexpr int kSize = V * (FP32 ? 4 : 2);
+    std::conditional_t<V == 1, uint32_t, uint4> w;
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int g) {
+        if constexpr (V > 1) w = bload16_nt(r, g * kSize);
+        else if constexpr (FP32) w = __builtin_amdgcn_raw_buffer_load_b32(r, g * kSize, 0, 0);
+        else w = __builtin_amdgcn_raw_buffer_load_b16(r, g * kSize, 0, 0);
+    }
+    __device__ __forceinline__ void values(float (&f)[V]) const {
+        if constexpr (V == 1) {
+            f[0] = __uint_as_float(FP32 ? w : w << 16);
+        } else {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (FP32) f[j] = __uint_as_float(u[j]);
+                else f[2 * j] = bf16_lo(u[j]), f[2 * j + 1] = bf16_hi(u[j]);
+            }
+        }
+    }
+};
+
+// V values as fp32 or bf16; AUX: cache policy.
+template <bool FP32, int AUX, int V>
+__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, int g, const float (&f)[V]) {
+    const int at = g * V * (FP32 ? 4 : 2);
     if constexpr (V == 1) {
-        if constexpr (FP32) f[0] = reinterpret_cast<const float *>(p)[at];
-        else f[0] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[at] << 16);
+        if constexpr (FP32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(f[0], 0.0f), r, at, 0, 0);
     } else if constexpr (FP32) {
-        const v4f *s = reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(p) + at);
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) {
-            const v4f a = __builtin_nontemporal_load(s + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[4 * i + j] = a[j];
+            const v4f v{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at + 16 * i, 0, AUX);
         }
+    } else if constexpr (V == 8) {
+        const u32x4 w{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                      pack_bf16(f[6], f[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, at, 0, AUX);
     } else {
-        const u32x4 w = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p) + at));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+        const u32x2 w{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, at, 0, AUX);
     }
 }
 
-template <bool FP32, bool KEEP, int V>
-__device__ __forceinline__ void store_piece(void *p, int64_t at, const float (&f)[V]) {
-    auto put = [](auto v, auto *o) {
-        if constexpr (KEEP || V == 1) *o = v;
-        else __builtin_nontemporal_store(v, o);
-    };
-    if constexpr (V == 1) {
-        if constexpr (FP32) put(f[0], reinterpret_cast<float *>(p) + at);
-        else put((uint16_t)pack_bf16(f[0], 0.0f), reinterpret_cast<uint16_t *>(p) + at);
-    } else if constexpr (FP32) {
-        v4f *o = reinterpret_cast<v4f *>(reinterpret_cast<float *>(p) + at);
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-            put(v4f{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}, o + i);
-    } else {
-        typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-        words w;
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-        put(w, reinterpret_cast<words *>(reinterpret_cast<uint16_t *>(p) + at));
-    }
-}
-
+// Pieces of 16 bytes of x, or single values (V = 1) where K, a stride or an address
+// does not allow those: thread t owns pieces t, t + T, ... (NG), all loads issued at
+// once, neighbouring lanes side by side in every array; a row is read once and stays
+// in registers.  x and the residual are read, and the sum written, past the caches,
+// whose place the output has for the product that takes it (8192 rows of 8192, fp32
+// with residual to bf16, 940 MB: 141 us, 6.7 TB/s; the output past them too 152, all
+// through them 160; one row of 1152 to int8 2.1 us, 64 rows of 4096 with residual 3.5;
+// single values: 8192 rows of 4097 bf16 65, waiting for each load 142).
 // Rows of one wave (T = 64) share a workgroup of four and no barrier.
 template <bool FP32, int OUT, bool RES, int V, int T, int NG>
 __global__ __launch_bounds__(T > 256 ? T : 256) void k_rms_norm(NormArgs a) {
     constexpr int kWaves = T / kWave, kRows = T > kWave ? 1 : 4;
+    constexpr int kX = FP32 ? 4 : 2, kOut = OUT == kNormInt8 ? 1 : OUT == RMS_FP32 ? 4 : 2;
     __shared__ double red[kWaves];
     __shared__ uint32_t redm[kWaves];
-    const int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / T, K = a.K;
+    const int in_group = kRows > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+    const int64_t m = (int64_t)blockIdx.x * kRows + in_group, K = a.K;
     const int tid = threadIdx.x % T;
     if (kRows > 1 && m >= a.M) return;
-    const int ng = (int)K / V;
-    float h[NG][V], r[NG][V], w[NG][V];
+    const auto rx = make_rsrc(reinterpret_cast<const uint8_t *>(a.x) + m * a.ldx * kX, K * kX);
+    const auto rr = make_rsrc(reinterpret_cast<const uint8_t *>(a.res) + m * K * kX, K * kX);
+    const auto rs = make_rsrc(reinterpret_cast<const uint8_t *>(a.sum) + m * K * kX, K * kX);
+    const auto ro = make_rsrc(reinterpret_cast<const uint8_t *>(a.out) + m * K * kOut, K * kOut);
+    const auto rw = make_rsrc(a.weight, a.weight ? K * 4 : 0);
+    Piece<FP32, V> x[NG], r[NG];
+    float w[NG][V];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-        const int g = tid + T * u;
+        x[u].load(rx, tid + T * u);
+        if constexpr (RES) r[u].load(rr, tid + T * u);
+    }
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[u][j] = 0.0f, r[u][j] = 0.0f, w[u][j] = 1.0f;
-        if (g >= ng) continue;
-        load_piece<FP32>(a.x, m * a.ldx + V * g, h[u]);
-        if constexpr (RES) load_piece<FP32>(a.res, m * K + V * g, r[u]);
-        if (a.weight) {
-            if constexpr (V == 1) w[u][0] = a.weight[g];
+    for (int u = 0; u < NG; ++u) {
+        const int at = (tid + T * u) * V * 4;
+        if constexpr (V == 1) w[u][0] = bloadf(rw, at);
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 p = reinterpret_cast<const float4 *>(a.weight + V * g)[i];
-                w[u][4 * i] = p.x, w[u][4 * i + 1] = p.y, w[u][4 * i + 2] = p.z, w[u][4 * i + 3] = p.w;
-            }
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 p = bloadf4(rw, at + 16 * i);
+            w[u][4 * i] = p.x, w[u][4 * i + 1] = p.y, w[u][4 * i + 2] = p.z, w[u][4 * i + 3] = p.w;
         }
     }
+    float h[NG][V];
     double ss = 0.0;
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-        const int g = tid + T * u;
+        x[u].values(h[u]);
         if constexpr (RES) {
+            float f[V];
+            r[u].values(f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) h[u][j] += r[u][j];
-            if (g < ng) store_piece<FP32, false>(a.sum, m * K + V * g, h[u]);
+            for (int j = 0; j < V; ++j) h[u][j] += f[j];
+            store_piece<FP32, kNonTemporal>(rs, tid + T * u, h[u]);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -227,49 +243,45 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void k_rms_norm(NormArgs a) {
 #pragma unroll
     for (int u = 0; u < NG; ++u)
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[u][j] = (h[u][j] * s) * (a.offset + w[u][j]);
+        for (int j = 0; j < V; ++j) h[u][j] = (h[u][j] * s) * (a.offset + (a.weight ? w[u][j] : 1.0f));
     if constexpr (OUT == kNormInt8) {
+        // (beyond the row y is zero, or NaN as the row's own values are)
         uint32_t top = 0;
 #pragma unroll
         for (int u = 0; u < NG; ++u)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (tid + T * u < ng) top = max(top, abs_bits(h[u][j]));
+            for (int j = 0; j < V; ++j) top = max(top, abs_bits(h[u][j]));
         const float sx = row_scale_of<kWaves>(top, redm);
         if (tid == 0) a.sx[m] = sx;
         auto codes = [&](auto code) {
 #pragma unroll
             for (int u = 0; u < NG; ++u) {
-                const int g = tid + T * u;
-                if (g >= ng) continue;
-                int8_t *o = reinterpret_cast<int8_t *>(a.out) + m * K + V * g;
+                const int at = (tid + T * u) * V;
                 const float(&f)[V] = h[u];
                 if constexpr (V == 1) {
-                    *o = (int8_t)code(f[0]);
+                    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)code(f[0]), ro, at, 0, 0);
                 } else {
                     uint32_t c[V / 4];
 #pragma unroll
                     for (int i = 0; i < V / 4; ++i)
                         c[i] = pack4_i8(code(f[4 * i]), code(f[4 * i + 1]), code(f[4 * i + 2]),
                                         code(f[4 * i + 3]));
-                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(o) = uint2{c[0], c[1]};
-                    else *reinterpret_cast<uint32_t *>(o) = c[0];
+                    if constexpr (V == 8)
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, ro, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b32(c[0], ro, at, 0, 0);
                 }
             }
         };
         if (sx >= kFastQuotientMinScale) {
-            const float rs = 1.0f / sx;
-            codes([&](float x) { return (int)code_in_low_byte(quotient_rn(x, sx, rs)); });
+            const float inv = 1.0f / sx;
+            codes([&](float v) { return (int)code_in_low_byte(quotient_rn(v, sx, inv)); });
         } else {  // zero, tiny or NaN
             const RowScale q = row_scale(sx);
-            codes([&](float x) { return quant_code_row(x, q); });
+            codes([&](float v) { return quant_code_row(v, q); });
         }
     } else {
 #pragma unroll
-        for (int u = 0; u < NG; ++u) {
-            const int g = tid + T * u;
-            if (g < ng) store_piece<OUT == RMS_FP32, true>(a.out, m * K + V * g, h[u]);
-        }
+        for (int u = 0; u < NG; ++u) store_piece<OUT == RMS_FP32, 0>(ro, tid + T * u, h[u]);
     }
 }
 
