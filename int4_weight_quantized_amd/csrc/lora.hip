@@ -20,6 +20,8 @@
 
 namespace w4 {
 
+template <int N> using Int = std::integral_constant<int, N>;
+
 struct LoraPlan {
     int slots, splits, kc;  // workgroups of a tile, parts of K, length of a part
     int rp;                 // rank, rounded up to 16: a row of S
@@ -75,30 +77,6 @@ __device__ __forceinline__ void cut3(const float (&f)[8], v8bf (&out)[3]) {
     }
 }
 
-// Eight bf16 from p (aligned to 2 bytes), the first `n` of them valid, zeros for
-// the others: whole pieces while there are some, the rest one by one.
-__device__ __forceinline__ uint4 some8(const uint16_t *p, int n) {
-    uint4 v{};
-    if (n >= 8) {
-        __builtin_memcpy(&v, p, 16);
-        return v;
-    }
-    uint32_t w[8] = {};
-    int j = 0;
-    if (n >= 4) {
-        uint2 u;
-        __builtin_memcpy(&u, p, 8);
-        v.x = u.x, v.y = u.y;
-        j = 4;
-    }
-#pragma unroll
-    for (int e = 0; e < 3; ++e) w[e] = j + e < n ? p[j + e] : 0u;
-    const uint32_t lo = w[0] | w[1] << 16, hi = w[2];
-    if (n >= 4) v.z = lo, v.w = hi;
-    else v.x = lo, v.y = hi;
-    return v;
-}
-
 // Which of eight bf16 to keep, the first `n` (the others may hold anything).
 __device__ __forceinline__ uint4 keep8(int n) {
     auto two = [&](int i) { return n > i + 1 ? ~0u : n > i ? 0xFFFFu : 0u; };
@@ -109,19 +87,32 @@ __device__ __forceinline__ uint4 and8(uint4 w, uint4 k) {
     return uint4{w.x & k.x, w.y & k.y, w.z & k.z, w.w & k.w};
 }
 
-// Eight values of X as operand terms.
+__device__ __forceinline__ uint4 not8(uint4 k) { return uint4{~k.x, ~k.y, ~k.z, ~k.w}; }
+
+// Eight bf16 at an offset that is aligned to 2 bytes; zeros outside the range.
+__device__ __forceinline__ uint4 bload8x2(__amdgpu_buffer_rsrc_t r, int off) {
+    uint32_t f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * j, 0, 0);
+    return uint4{f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16, f[6] | f[7] << 16};
+}
+
+// Eight values of X, or of A, as operand terms: from p, aligned to its elements, or
+// values k, k + 1, ... of a row of `end` (1 or more) and zeros beyond it; no load is in
+// a branch.
 template <bool FP32> struct Chunk;
 template <> struct Chunk<true> {
     float4 a, b;
-    __device__ __forceinline__ void some(const float *p, int n) {
-        if (n >= 8) {
-            __builtin_memcpy(&a, p, 16);
-            __builtin_memcpy(&b, p + 4, 16);
-            return;
-        }
+    __device__ __forceinline__ void whole(const float *p) {
+        __builtin_memcpy(&a, p, 16);
+        __builtin_memcpy(&b, p + 4, 16);
+    }
+    __device__ __forceinline__ void some(const float *row, int k, int end) {
         float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = j < n ? p[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) f[j] = row[min(k + j, end - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = k + j < end ? f[j] : 0.0f;
         a = float4{f[0], f[1], f[2], f[3]}, b = float4{f[4], f[5], f[6], f[7]};
     }
     __device__ __forceinline__ void terms(v8bf (&out)[3]) const {
@@ -131,7 +122,14 @@ template <> struct Chunk<true> {
 };
 template <> struct Chunk<false> {
     uint4 w;
-    __device__ __forceinline__ void some(const uint16_t *p, int n) { w = some8(p, n); }
+    __device__ __forceinline__ void whole(const uint16_t *p) { __builtin_memcpy(&w, p, 16); }
+    __device__ __forceinline__ void some(const uint16_t *row, int k, int end) {
+        uint32_t f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = row[min(k + j, end - 1)];
+        w = and8(uint4{f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16, f[6] | f[7] << 16},
+                 keep8(end - k));
+    }
     __device__ __forceinline__ void terms(v8bf (&out)[1]) const { out[0] = __builtin_bit_cast(v8bf, w); }
 };
 
@@ -160,7 +158,9 @@ __device__ __forceinline__ void write_sums(const LoraArgs &a, const LoraPlan &p,
 // quarter of the part each and add their sums in LDS.  A is the first operand
 // and X the second, so that a lane ends with four neighbouring values of a row
 // of S.  X is read once (for every 16 RC ranks), straight into registers: this form
-// takes every size and alignment (409 rows 451 -> 6342, rank 29: 8 us).
+// takes every size and alignment: whole steps of 32 k by loads aligned to elements, a
+// last one value by value, with no branch between the loads (409 rows of 451, rank 29:
+// 6.8 us, with branches 7.9).
 template <bool FP32, int MT, int RC>
 __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
     constexpr int U = FP32 ? 4 / MT : MT * RC >= 8 ? 1 : 8 / (MT * RC);  // k-steps in flight
@@ -180,44 +180,54 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
         if (r0 >= rank) return;
         const int ranks = min(rank - r0, 16 * RC);
         const uint16_t *A = a.A + ((int64_t)cur * a.rank + r0) * a.K;
+        // (a lane without a row of X or of A reads the first one: what comes of it is no
+        // row's, or is dropped)
+        const X *x[MT];
+        const uint16_t *w[RC];
         v4f acc[MT][RC];
-        bool on[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            on[t] = match >> (16 * t + c16) & 1;
+            x[t] = rows + (match >> (16 * t + c16) & 1 ? 16 * t + c16 : 0) * a.ldx;
 #pragma unroll
             for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
         }
-        for (int k = k0; k < k1; k += 32 * U) {
-            Chunk<FP32> x[U][MT];
-            uint4 w[U][RC];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int c = 0; c < RC; ++c)
+            w[c] = A + (int64_t)(16 * c + c16 < ranks ? 16 * c + c16 : 0) * K;
+        // `steps` k-steps from k; whole: all of their values are the part's
+        auto add = [&](int k, auto steps, auto whole) {
+            constexpr int kSteps = decltype(steps)::value;
+            Chunk<FP32> xs[kSteps][MT];
+            Chunk<false> ws[kSteps][RC];
+            auto load = [&](auto &chunk, auto *row, int at) {
+                if constexpr (decltype(whole)::value) chunk.whole(row + at);
+                else chunk.some(row, at, k1);
+            };
 #pragma unroll
-                for (int c = 0; c < RC; ++c) {
-                    const int kk = k + 32 * u + q8, j = 16 * c + c16;
-                    w[u][c] = some8(A + (int64_t)j * K + kk, j < ranks ? k1 - kk : 0);
-                }
+            for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
+                for (int c = 0; c < RC; ++c) load(ws[u][c], w[c], k + 32 * u + q8);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int kk = k + 32 * u + q8;
-                    x[u][t].some(rows + (16 * t + c16) * a.ldx + kk, on[t] ? k1 - kk : 0);
-                }
+            for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int t = 0; t < MT; ++t) load(xs[u][t], x[t], k + 32 * u + q8);
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     v8bf f[kTerms];
-                    x[u][t].terms(f);
+                    xs[u][t].terms(f);
 #pragma unroll
                     for (int c = 0; c < RC; ++c)
 #pragma unroll
                         for (int i = kTerms - 1; i >= 0; --i)
-                            acc[t][c] = mfma(__builtin_bit_cast(v8bf, w[u][c]), f[i], acc[t][c]);
+                            acc[t][c] = mfma(__builtin_bit_cast(v8bf, ws[u][c].w), f[i], acc[t][c]);
                 }
-        }
+        };
+        int k = k0;
+        for (; k + 32 * U <= k1; k += 32 * U) add(k, Int<U>{}, std::true_type{});
+        for (; k + 32 <= k1; k += 32) add(k, Int<1>{}, std::true_type{});
+        if (k < k1) add(k, Int<1>{}, std::false_type{});
         lds_barrier();  // (the sums of the adapter before have been read)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -351,7 +361,8 @@ __global__ __launch_bounds__(256) void k_lora_down_lds(LoraArgs a, LoraPlan p) {
 // channels of a row).  The 256 channels of the four waves change lanes in LDS, so
 // that Y is read and written in whole pieces of 1 KB of a row, and only its own rows;
 // in tiles of 32 rows, those of prompts, past the caches (8192 rows, K = N = 4096,
-// rank 32, both launches: 90 -> 85 us).
+// rank 32, both launches: 90 -> 85 us).  Without VEC, B's pieces may lie anywhere (16
+// rows -> 28671, rank 61: 20.4 us, 13.5 where aligned; value by value 44).
 template <bool VEC, bool YVEC, int MT, int KS>
 __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
     constexpr int NU = 4;  // blocks of 16 channels whose loads are in flight
@@ -371,25 +382,38 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
         const float scale = a.scales ? a.scales[cur] : 1.0f;
         const uint16_t *B = a.B + ((int64_t)cur * a.N + n0) * a.rank;
         const auto rb = make_rsrc(B, (int64_t)len * a.rank * 2);  // (beyond it: zeros)
-        int at[KS];  // this lane's bytes of a block of 16 channels
+        // This lane's ranks of step s: 32 s + 8 q and the 7 behind it.  Where pieces may not
+        // be aligned, a row's last piece is the 8 that end it, of which those that an
+        // earlier piece has are dropped, so that every load is whole and within its row.
+        int first[KS], at[KS];  // rank of a piece's first value; its bytes in a block of 16 channels
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int j = 32 * s + 8 * q;
+            first[s] = VEC || a.rank < 8 ? j : min(j, a.rank - 8);
             // (the pool's rank, so that no load waits for the adapter's own)
             at[s] = j < a.rank ? (c16 * a.rank + j) * 2 : kOOB;
         }
         uint4 w[NU][KS];
         v4f y[4 * MT];  // of rows wave, wave + 4, ...: this lane's four channels of 256
-        auto load_b = [&](int n) {
+        auto load_b = [&](int n, auto load) {
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int ch = n + 64 * wave + 16 * u;
-                    if constexpr (VEC) w[u][s] = bload16(rb, (int)((uint32_t)at[s] + (uint32_t)(ch * a.rank * 2)));
-                    else w[u][s] = some8(B + (int64_t)(ch + c16) * a.rank + 32 * s + 8 * q,
-                                         ch + c16 < len ? rank - 32 * s - 8 * q : 0);
-                }
+                for (int s = 0; s < KS; ++s) w[u][s] = load(n + 64 * wave + 16 * u, s);
+        };
+        auto load_channels = [&](int n) {
+            auto offset = [&](int ch, int s) { return (int)((uint32_t)at[s] + (uint32_t)(ch * a.rank * 2)); };
+            if constexpr (VEC) {
+                load_b(n, [&](int ch, int s) { return bload16(rb, offset(ch, s)); });
+            } else if (a.rank >= 8) {
+                load_b(n, [&](int ch, int s) {
+                    uint4 v;
+                    __builtin_memcpy(&v, B + min(ch + c16, len - 1) * a.rank + first[s], 16);
+                    return v;
+                });
+            } else {
+                load_b(n, [&](int ch, int s) { return bload8x2(rb, offset(ch, s)); });
+            }
         };
         // this lane's channels: 4 lane + e, or lane + 64 e where Y goes value by value
         auto channel = [&](int e) { return YVEC ? 4 * lane + e : lane + 64 * e; };
@@ -424,12 +448,15 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
         };
         auto read = [&](int i, int, auto get, auto) { get(y[i]); };
         int n = 0;
-        load_b(n);  // (in flight while S is summed)
+        load_channels(n);  // (in flight while S is summed)
         each_y(n, read);
         if (rank == 0) return;
         uint4 keep[KS];  // which values of a lane's pieces count
 #pragma unroll
-        for (int s = 0; s < KS; ++s) keep[s] = keep8(rank - 32 * s - 8 * q);
+        for (int s = 0; s < KS; ++s) {
+            keep[s] = keep8(rank - first[s]);
+            if constexpr (!VEC) keep[s] = and8(keep[s], not8(keep8(32 * s + 8 * q - first[s])));
+        }
         lds_barrier();  // (the rows of the adapter before have been read)
         const int64_t part = a.M * p.rp;
         for (int i = threadIdx.x; i < 16 * MT * 8 * KS; i += 256) {
@@ -459,9 +486,9 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 float v[8];
-                const float *src = &S[16 * t + c16][32 * s + 8 * q];
+                const float *src = &S[16 * t + c16][first[s]];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = src[e];
+                for (int e = 0; e < 8; ++e) v[e] = VEC || first[s] + e >= 32 * s + 8 * q ? src[e] : 0.0f;
                 cut3(v, f[t][s]);
             }
         for (;;) {
@@ -475,11 +502,10 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
                     for (int s = 0; s < KS; ++s)
 #pragma unroll
                         for (int i = 2; i >= 0; --i)
-                            acc = mfma(__builtin_bit_cast(v8bf, VEC ? and8(w[u][s], keep[s]) : w[u][s]),
-                                       f[t][s][i], acc);
+                            acc = mfma(__builtin_bit_cast(v8bf, and8(w[u][s], keep[s])), f[t][s][i], acc);
                     *reinterpret_cast<v4f *>(&D[16 * t + c16][64 * wave + 16 * u + 4 * q]) = acc;
                 }
-            if (next < len) load_b(next);
+            if (next < len) load_channels(next);
             lds_barrier();
             each_y(n, [&](int i, int m, auto, auto put) {
                 v4f v;

@@ -131,6 +131,26 @@ def test_what_takes_no_part_may_hold_anything(M, dt):
     assert torch.equal(w4.lora_add(Y.clone(), X, ids, A, B, ranks=-big), Y)
 
 
+@pytest.mark.parametrize("r", [3, 7, 8, 9, 15, 31, 33, 61, 100, 127, 201, 255])
+@pytest.mark.parametrize("M,K", [(4, 97), (60, 131), (260, 300)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_pieces_that_share_ranks(r, M, K, dt):
+    """Ranks and lengths that end inside a piece of 8, with NaN behind each adapter's
+    own rank, in a row without an adapter, and in the first row of a tile."""
+    N, own = 139, [r, r - 1, 1, max(r - 8, 1), max(r - 9, 2), 0]
+    X, A, B, scales, ids, _, Y = make(M, K, N, r, 6, dt, M + r)
+    ids = (torch.arange(M) % 7 - 1).int()  # (row 0 has none)
+    ranks = torch.tensor(own, dtype=torch.int32)
+    want, bound = formula(X, A, B, scales, ids, ranks, Y)
+    for a, n in enumerate(own):
+        A[a, n:], B[a, :, n:] = math.nan, math.nan
+    X[ids < 0] = math.nan
+    c = cuda(X, A, B, scales, ids, ranks)
+    y = w4.lora_add(Y.cuda(), c[0], c[4], c[1], c[2], scales=c[3], ranks=c[5])
+    close(y, want, bound)
+    assert torch.equal(y.cpu()[ids < 0], Y[ids < 0])
+
+
 @pytest.mark.parametrize("M,r", [(2, 8), (50, 16), (300, 20)])
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_strided_and_shifted(M, r, dt):
