@@ -621,7 +621,8 @@ int rope_rotate(const rope_spec *rope, const void *x, int x_dtype, int64_t x_str
  *            sequence and of skipped ones (start[b] < 0) keep what q_out held.
  *   k        rotated in fp32, then rounded or quantized into the cache;
  *   v        as in kv_append; everything else too.
- * T * (q_heads + 2 * heads) <= 2^26; head_dim not below rot_dim.
+ * T <= 2^23, q_heads <= 65535, T * (q_heads + 2 * heads) <= 2^26; head_dim not below
+ * rot_dim.
  * Returns W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ARG, W4_ERR_ALIGN or W4_ERR_HIP. */
 int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, const void *q,
                    const void *k, const void *v, int x_dtype, int64_t q_stride, int64_t k_stride,
