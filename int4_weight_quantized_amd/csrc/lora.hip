@@ -172,70 +172,70 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraArgs a, LoraPlan p) {
     const int K = (int)a.K, r0 = blockIdx.z * (16 * RC);
     const int kw = p.kc / 4, k0 = blockIdx.x * p.kc + wave * kw, k1 = min(k0 + kw, K);
     for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
-    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
-    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
-    const X *rows = reinterpret_cast<const X *>(a.X) + m0 * a.ldx;
-    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
-        const int rank = lora_rank(a, cur);
-        if (r0 >= rank) return;
-        const int ranks = min(rank - r0, 16 * RC);
-        const uint16_t *A = a.A + ((int64_t)cur * a.rank + r0) * a.K;
-        // (a lane without a row of X or of A reads the first one: what comes of it is no
-        // row's, or is dropped)
-        const X *x[MT];
-        const uint16_t *w[RC];
-        v4f acc[MT][RC];
+        const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+        const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+        const X *rows = reinterpret_cast<const X *>(a.X) + m0 * a.ldx;
+        each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
+            const int rank = lora_rank(a, cur);
+            if (r0 >= rank) return;
+            const int ranks = min(rank - r0, 16 * RC);
+            const uint16_t *A = a.A + ((int64_t)cur * a.rank + r0) * a.K;
+            // (a lane without a row of X or of A reads the first one: what comes of it is no
+            // row's, or is dropped)
+            const X *x[MT];
+            const uint16_t *w[RC];
+            v4f acc[MT][RC];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            x[t] = rows + (match >> (16 * t + c16) & 1 ? 16 * t + c16 : 0) * a.ldx;
+            for (int t = 0; t < MT; ++t) {
+                x[t] = rows + (match >> (16 * t + c16) & 1 ? 16 * t + c16 : 0) * a.ldx;
 #pragma unroll
-            for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
+                for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+            }
 #pragma unroll
-        for (int c = 0; c < RC; ++c)
-            w[c] = A + (int64_t)(16 * c + c16 < ranks ? 16 * c + c16 : 0) * K;
-        // `steps` k-steps from k; whole: all of their values are the part's
-        auto add = [&](int k, auto steps, auto whole) {
-            constexpr int kSteps = decltype(steps)::value;
-            Chunk<FP32> xs[kSteps][MT];
-            Chunk<false> ws[kSteps][RC];
-            auto load = [&](auto &chunk, auto *row, int at) {
-                if constexpr (decltype(whole)::value) chunk.whole(row + at);
-                else chunk.some(row, at, k1);
+            for (int c = 0; c < RC; ++c)
+                w[c] = A + (int64_t)(16 * c + c16 < ranks ? 16 * c + c16 : 0) * K;
+            // `steps` k-steps from k; whole: all of their values are the part's
+            auto add = [&](int k, auto steps, auto whole) {
+                constexpr int kSteps = decltype(steps)::value;
+                Chunk<FP32> xs[kSteps][MT];
+                Chunk<false> ws[kSteps][RC];
+                auto load = [&](auto &chunk, auto *row, int at) {
+                    if constexpr (decltype(whole)::value) chunk.whole(row + at);
+                    else chunk.some(row, at, k1);
+                };
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                    for (int c = 0; c < RC; ++c) load(ws[u][c], w[c], k + 32 * u + q8);
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) load(xs[u][t], x[t], k + 32 * u + q8);
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        v8bf f[kTerms];
+                        xs[u][t].terms(f);
+#pragma unroll
+                        for (int c = 0; c < RC; ++c)
+#pragma unroll
+                            for (int i = kTerms - 1; i >= 0; --i)
+                                acc[t][c] = mfma(__builtin_bit_cast(v8bf, ws[u][c].w), f[i], acc[t][c]);
+                    }
             };
+            int k = k0;
+            for (; k + 32 * U <= k1; k += 32 * U) add(k, Int<U>{}, std::true_type{});
+            for (; k + 32 <= k1; k += 32) add(k, Int<1>{}, std::true_type{});
+            if (k < k1) add(k, Int<1>{}, std::false_type{});
+            lds_barrier();  // (the sums of the adapter before have been read)
 #pragma unroll
-            for (int u = 0; u < kSteps; ++u)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int c = 0; c < RC; ++c) load(ws[u][c], w[c], k + 32 * u + q8);
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) load(xs[u][t], x[t], k + 32 * u + q8);
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    v8bf f[kTerms];
-                    xs[u][t].terms(f);
-#pragma unroll
-                    for (int c = 0; c < RC; ++c)
-#pragma unroll
-                        for (int i = kTerms - 1; i >= 0; --i)
-                            acc[t][c] = mfma(__builtin_bit_cast(v8bf, ws[u][c].w), f[i], acc[t][c]);
-                }
-        };
-        int k = k0;
-        for (; k + 32 * U <= k1; k += 32 * U) add(k, Int<U>{}, std::true_type{});
-        for (; k + 32 <= k1; k += 32) add(k, Int<1>{}, std::true_type{});
-        if (k < k1) add(k, Int<1>{}, std::false_type{});
-        lds_barrier();  // (the sums of the adapter before have been read)
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
-        lds_barrier();
-        write_sums<MT, RC>(a, p, red, m0, r0, match);
-    });
+                for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
+            lds_barrier();
+            write_sums<MT, RC>(a, p, red, m0, r0, match);
+        });
     }
 }
 
@@ -263,94 +263,94 @@ __global__ __launch_bounds__(256) void k_lora_down_lds(LoraArgs a, LoraPlan p) {
     const int k0 = blockIdx.x * p.kc, k1 = min(k0 + p.kc, K);
     const uint32_t base = lds_addr(lds);
     for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
-    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
-    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
-    const v4i rx = buffer_desc(reinterpret_cast<const uint8_t *>(a.X) + m0 * a.ldx * (FP32 ? 4 : 2),
-                               kMaxRange);
-    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
-        const int rank = lora_rank(a, cur);
-        if (r0 >= rank) return;
-        const int ranks = min(rank - r0, 16 * RC);
-        const v4i ra = buffer_desc(a.A + ((int64_t)cur * a.rank + r0) * a.K,
-                                   (int64_t)ranks * a.K * 2);
-        // this lane's piece of each of the wave's loads: byte offset at k = 0, and its k
-        constexpr int kXPieces = kXRow / 16, kAPieces = kARow / 16;
-        int xoff[kXLoads], xk[kXLoads], aoff[kALoads], ak[kALoads];
+        const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+        const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+        const v4i rx = buffer_desc(reinterpret_cast<const uint8_t *>(a.X) + m0 * a.ldx * (FP32 ? 4 : 2),
+                                   kMaxRange);
+        each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
+            const int rank = lora_rank(a, cur);
+            if (r0 >= rank) return;
+            const int ranks = min(rank - r0, 16 * RC);
+            const v4i ra = buffer_desc(a.A + ((int64_t)cur * a.rank + r0) * a.K,
+                                       (int64_t)ranks * a.K * 2);
+            // this lane's piece of each of the wave's loads: byte offset at k = 0, and its k
+            constexpr int kXPieces = kXRow / 16, kAPieces = kARow / 16;
+            int xoff[kXLoads], xk[kXLoads], aoff[kALoads], ak[kALoads];
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i) {
-            const int n = (wave * kXLoads + i) * kWave + lane, m = n / kXPieces;
-            xk[i] = ((n % kXPieces) ^ (m % 16)) * (FP32 ? 4 : 8);
-            xoff[i] = match >> m & 1 ? (int)(m * a.ldx + xk[i]) * (FP32 ? 4 : 2) : kOOB;
-        }
-#pragma unroll
-        for (int i = 0; i < kALoads; ++i) {
-            const int n = (wave * kALoads + i) * kWave + lane, j = n / kAPieces;
-            ak[i] = ((n % kAPieces) ^ (j % 16)) * 8;
-            aoff[i] = j < ranks ? (j * K + ak[i]) * 2 : kOOB;
-        }
-        auto fetch = [&](int k, int slot) {
-            const uint32_t to = base + slot * kBytes;
-#pragma unroll
-            for (int i = 0; i < kXLoads; ++i)
-                dma16_nt(rx, to + (wave * kXLoads + i) * 1024,
-                      k + xk[i] < k1 && xoff[i] != kOOB ? xoff[i] + k * (FP32 ? 4 : 2) : kOOB, 0);
-#pragma unroll
-            for (int i = 0; i < kALoads; ++i)
-                dma16(ra, to + kXBytes + (wave * kALoads + i) * 1024,
-                      k + ak[i] < k1 && aoff[i] != kOOB ? aoff[i] + k * 2 : kOOB, 0);
-        };
-        v4f acc[MT][RC];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
-        wait_and_barrier<0>();  // (LDS is free, and no store is counted among the loads)
-        fetch(k0, 0);
-        if (k0 + kStage < k1) fetch(k0 + kStage, 1);
-        int slot = 0;
-        for (int k = k0; k < k1; k += kStage) {
-            if (k + kStage < k1) wait_and_barrier<kLoads>();
-            else wait_and_barrier<0>();
-            if (k + 2 * kStage < k1) fetch(k + 2 * kStage, slot == 0 ? 2 : slot - 1);
-            const uint8_t *from = lds + slot * kBytes;
-            const int kk = k + 32 * wave + 8 * q;
-            uint4 w[RC];
-#pragma unroll
-            for (int c = 0; c < RC; ++c) {
-                w[c] = *reinterpret_cast<const uint4 *>(from + kXBytes + (16 * c + c16) * kARow +
-                                                        ((4 * wave + q) ^ c16) * 16);
-                if (kk >= k1) w[c] = uint4{};
+            for (int i = 0; i < kXLoads; ++i) {
+                const int n = (wave * kXLoads + i) * kWave + lane, m = n / kXPieces;
+                xk[i] = ((n % kXPieces) ^ (m % 16)) * (FP32 ? 4 : 8);
+                xoff[i] = match >> m & 1 ? (int)(m * a.ldx + xk[i]) * (FP32 ? 4 : 2) : kOOB;
             }
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const uint8_t *row = from + (16 * t + c16) * kXRow;
-                Chunk<FP32> x;
-                if constexpr (FP32) {
-                    x.a = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q) ^ c16) * 16);
-                    x.b = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q + 1) ^ c16) * 16);
-                } else {
-                    x.w = *reinterpret_cast<const uint4 *>(row + ((4 * wave + q) ^ c16) * 16);
+            for (int i = 0; i < kALoads; ++i) {
+                const int n = (wave * kALoads + i) * kWave + lane, j = n / kAPieces;
+                ak[i] = ((n % kAPieces) ^ (j % 16)) * 8;
+                aoff[i] = j < ranks ? (j * K + ak[i]) * 2 : kOOB;
+            }
+            auto fetch = [&](int k, int slot) {
+                const uint32_t to = base + slot * kBytes;
+#pragma unroll
+                for (int i = 0; i < kXLoads; ++i)
+                    dma16_nt(rx, to + (wave * kXLoads + i) * 1024,
+                          k + xk[i] < k1 && xoff[i] != kOOB ? xoff[i] + k * (FP32 ? 4 : 2) : kOOB, 0);
+#pragma unroll
+                for (int i = 0; i < kALoads; ++i)
+                    dma16(ra, to + kXBytes + (wave * kALoads + i) * 1024,
+                          k + ak[i] < k1 && aoff[i] != kOOB ? aoff[i] + k * 2 : kOOB, 0);
+            };
+            v4f acc[MT][RC];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int c = 0; c < RC; ++c) acc[t][c] = v4f{0.f, 0.f, 0.f, 0.f};
+            wait_and_barrier<0>();  // (LDS is free, and no store is counted among the loads)
+            fetch(k0, 0);
+            if (k0 + kStage < k1) fetch(k0 + kStage, 1);
+            int slot = 0;
+            for (int k = k0; k < k1; k += kStage) {
+                if (k + kStage < k1) wait_and_barrier<kLoads>();
+                else wait_and_barrier<0>();
+                if (k + 2 * kStage < k1) fetch(k + 2 * kStage, slot == 0 ? 2 : slot - 1);
+                const uint8_t *from = lds + slot * kBytes;
+                const int kk = k + 32 * wave + 8 * q;
+                uint4 w[RC];
+#pragma unroll
+                for (int c = 0; c < RC; ++c) {
+                    w[c] = *reinterpret_cast<const uint4 *>(from + kXBytes + (16 * c + c16) * kARow +
+                                                            ((4 * wave + q) ^ c16) * 16);
+                    if (kk >= k1) w[c] = uint4{};
                 }
-                if (kk >= k1) x = Chunk<FP32>{};
-                v8bf f[kTerms];
-                x.terms(f);
 #pragma unroll
-                for (int c = 0; c < RC; ++c)
+                for (int t = 0; t < MT; ++t) {
+                    const uint8_t *row = from + (16 * t + c16) * kXRow;
+                    Chunk<FP32> x;
+                    if constexpr (FP32) {
+                        x.a = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q) ^ c16) * 16);
+                        x.b = *reinterpret_cast<const float4 *>(row + ((8 * wave + 2 * q + 1) ^ c16) * 16);
+                    } else {
+                        x.w = *reinterpret_cast<const uint4 *>(row + ((4 * wave + q) ^ c16) * 16);
+                    }
+                    if (kk >= k1) x = Chunk<FP32>{};
+                    v8bf f[kTerms];
+                    x.terms(f);
 #pragma unroll
-                    for (int i = kTerms - 1; i >= 0; --i)
-                        acc[t][c] = mfma(__builtin_bit_cast(v8bf, w[c]), f[i], acc[t][c]);
+                    for (int c = 0; c < RC; ++c)
+#pragma unroll
+                        for (int i = kTerms - 1; i >= 0; --i)
+                            acc[t][c] = mfma(__builtin_bit_cast(v8bf, w[c]), f[i], acc[t][c]);
+                }
+                slot = slot == kSlots - 1 ? 0 : slot + 1;
             }
-            slot = slot == kSlots - 1 ? 0 : slot + 1;
-        }
-        v4f(*red)[MT * RC][kWave] = reinterpret_cast<v4f(*)[MT * RC][kWave]>(lds);
-        lds_barrier();  // (every wave has read its last stage)
+            v4f(*red)[MT * RC][kWave] = reinterpret_cast<v4f(*)[MT * RC][kWave]>(lds);
+            lds_barrier();  // (every wave has read its last stage)
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
-        lds_barrier();
-        write_sums<MT, RC>(a, p, red, m0, r0, match);
-    });
+                for (int c = 0; c < RC; ++c) red[wave][t * RC + c][lane] = acc[t][c];
+            lds_barrier();
+            write_sums<MT, RC>(a, p, red, m0, r0, match);
+        });
     }
 }
 
@@ -374,151 +374,151 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraArgs a, LoraPlan p) {
     const int64_t n0 = (int64_t)blockIdx.x * p.nc;
     const int len = (int)min((int64_t)p.nc, a.N - n0);
     for (uint32_t tile = blockIdx.y; tile < (uint32_t)(p.tiles * p.slots); tile += gridDim.y) {
-    const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
-    const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
-    float *rows = a.Y + m0 * a.ldy + n0;
-    each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
-        const int rank = lora_rank(a, cur);
-        const float scale = a.scales ? a.scales[cur] : 1.0f;
-        const uint16_t *B = a.B + ((int64_t)cur * a.N + n0) * a.rank;
-        const auto rb = make_rsrc(B, (int64_t)len * a.rank * 2);  // (beyond it: zeros)
-        // This lane's ranks of step s: 32 s + 8 q and the 7 behind it.  Where pieces may not
-        // be aligned, a row's last piece is the 8 that end it, of which those that an
-        // earlier piece has are dropped, so that every load is whole and within its row.
-        int first[KS], at[KS];  // rank of a piece's first value; its bytes in a block of 16 channels
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int j = 32 * s + 8 * q;
-            first[s] = VEC || a.rank < 8 ? j : min(j, a.rank - 8);
-            // (the pool's rank, so that no load waits for the adapter's own)
-            at[s] = j < a.rank ? (c16 * a.rank + j) * 2 : kOOB;
-        }
-        uint4 w[NU][KS];
-        v4f y[4 * MT];  // of rows wave, wave + 4, ...: this lane's four channels of 256
-        auto load_b = [&](int n, auto load) {
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) w[u][s] = load(n + 64 * wave + 16 * u, s);
-        };
-        auto load_channels = [&](int n) {
-            auto offset = [&](int ch, int s) { return (int)((uint32_t)at[s] + (uint32_t)(ch * a.rank * 2)); };
-            if constexpr (VEC) {
-                load_b(n, [&](int ch, int s) { return bload16(rb, offset(ch, s)); });
-            } else if (a.rank >= 8) {
-                load_b(n, [&](int ch, int s) {
-                    uint4 v;
-                    __builtin_memcpy(&v, B + min(ch + c16, len - 1) * a.rank + first[s], 16);
-                    return v;
-                });
-            } else {
-                load_b(n, [&](int ch, int s) { return bload8x2(rb, offset(ch, s)); });
-            }
-        };
-        // this lane's channels: 4 lane + e, or lane + 64 e where Y goes value by value
-        auto channel = [&](int e) { return YVEC ? 4 * lane + e : lane + 64 * e; };
-        auto each_y = [&](int n, auto f) {
-#pragma unroll
-            for (int i = 0; i < 4 * MT; ++i) {
-                const int m = wave + 4 * i;
-                if (!(match >> m & 1)) continue;
-                float *at = rows + m * a.ldy + n;
-                if constexpr (YVEC) {
-                    v4f *own = reinterpret_cast<v4f *>(at + 4 * lane);
-                    if (n + 4 * lane < len)
-                        f(i, m, [&](v4f &v) { v = MT > 1 ? __builtin_nontemporal_load(own) : *own; },
-                          [&](const v4f &v) {
-                              if constexpr (MT > 1) __builtin_nontemporal_store(v, own);
-                              else *own = v;
-                          });
-                } else {
-                    f(i, m,
-                      [&](v4f &v) {
-#pragma unroll
-                          for (int e = 0; e < 4; ++e)
-                              if (n + channel(e) < len) v[e] = at[channel(e)];
-                      },
-                      [&](const v4f &v) {
-#pragma unroll
-                          for (int e = 0; e < 4; ++e)
-                              if (n + channel(e) < len) at[channel(e)] = v[e];
-                      });
-                }
-            }
-        };
-        auto read = [&](int i, int, auto get, auto) { get(y[i]); };
-        int n = 0;
-        load_channels(n);  // (in flight while S is summed)
-        each_y(n, read);
-        if (rank == 0) return;
-        uint4 keep[KS];  // which values of a lane's pieces count
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            keep[s] = keep8(rank - first[s]);
-            if constexpr (!VEC) keep[s] = and8(keep[s], not8(keep8(32 * s + 8 * q - first[s])));
-        }
-        lds_barrier();  // (the rows of the adapter before have been read)
-        const int64_t part = a.M * p.rp;
-        for (int i = threadIdx.x; i < 16 * MT * 8 * KS; i += 256) {
-            const int m = i / (8 * KS), j = i % (8 * KS) * 4;
-            v4f s = v4f{0.f, 0.f, 0.f, 0.f};
-            if ((match >> m & 1) && j < rank) {
-                const float *src = a.ws + (m0 + m) * p.rp + j;
-                for (int k = 0; k < p.splits; k += 8) {  // (eight parts' loads at a time)
-                    v4f v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (k + e < p.splits)
-                            v[e] = *reinterpret_cast<const v4f *>(src + (k + e) * part);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (k + e < p.splits) s += v[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = j + e < rank ? s[e] : 0.0f;
-            }
-            *reinterpret_cast<v4f *>(&S[m][j]) = s;
-        }
-        lds_barrier();
-        v8bf f[MT][KS][3];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
+        const int64_t m0 = (int64_t)(tile % (uint32_t)p.tiles) * (16 * MT);
+        const int id = lane < 16 * MT ? lora_id(a, m0 + lane) : -1;
+        float *rows = a.Y + m0 * a.ldy + n0;
+        each_adapter(id, (int)(tile / (uint32_t)p.tiles), p.slots, [&](int cur, uint64_t match) {
+            const int rank = lora_rank(a, cur);
+            const float scale = a.scales ? a.scales[cur] : 1.0f;
+            const uint16_t *B = a.B + ((int64_t)cur * a.N + n0) * a.rank;
+            const auto rb = make_rsrc(B, (int64_t)len * a.rank * 2);  // (beyond it: zeros)
+            // This lane's ranks of step s: 32 s + 8 q and the 7 behind it.  Where pieces may not
+            // be aligned, a row's last piece is the 8 that end it, of which those that an
+            // earlier piece has are dropped, so that every load is whole and within its row.
+            int first[KS], at[KS];  // rank of a piece's first value; its bytes in a block of 16 channels
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                float v[8];
-                const float *src = &S[16 * t + c16][first[s]];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = VEC || first[s] + e >= 32 * s + 8 * q ? src[e] : 0.0f;
-                cut3(v, f[t][s]);
+                const int j = 32 * s + 8 * q;
+                first[s] = VEC || a.rank < 8 ? j : min(j, a.rank - 8);
+                // (the pool's rank, so that no load waits for the adapter's own)
+                at[s] = j < a.rank ? (c16 * a.rank + j) * 2 : kOOB;
             }
-        for (;;) {
-            const int next = n + 64 * NU;
+            uint4 w[NU][KS];
+            v4f y[4 * MT];  // of rows wave, wave + 4, ...: this lane's four channels of 256
+            auto load_b = [&](int n, auto load) {
 #pragma unroll
-            for (int u = 0; u < NU; ++u)
+                for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-#pragma unroll
-                        for (int i = 2; i >= 0; --i)
-                            acc = mfma(__builtin_bit_cast(v8bf, and8(w[u][s], keep[s])), f[t][s][i], acc);
-                    *reinterpret_cast<v4f *>(&D[16 * t + c16][64 * wave + 16 * u + 4 * q]) = acc;
+                    for (int s = 0; s < KS; ++s) w[u][s] = load(n + 64 * wave + 16 * u, s);
+            };
+            auto load_channels = [&](int n) {
+                auto offset = [&](int ch, int s) { return (int)((uint32_t)at[s] + (uint32_t)(ch * a.rank * 2)); };
+                if constexpr (VEC) {
+                    load_b(n, [&](int ch, int s) { return bload16(rb, offset(ch, s)); });
+                } else if (a.rank >= 8) {
+                    load_b(n, [&](int ch, int s) {
+                        uint4 v;
+                        __builtin_memcpy(&v, B + min(ch + c16, len - 1) * a.rank + first[s], 16);
+                        return v;
+                    });
+                } else {
+                    load_b(n, [&](int ch, int s) { return bload8x2(rb, offset(ch, s)); });
                 }
-            if (next < len) load_channels(next);
-            lds_barrier();
-            each_y(n, [&](int i, int m, auto, auto put) {
-                v4f v;
+            };
+            // this lane's channels: 4 lane + e, or lane + 64 e where Y goes value by value
+            auto channel = [&](int e) { return YVEC ? 4 * lane + e : lane + 64 * e; };
+            auto each_y = [&](int n, auto f) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(scale, D[m][channel(e)], y[i][e]);
-                put(v);
-            });
-            if (next >= len) break;
-            n = next;
+                for (int i = 0; i < 4 * MT; ++i) {
+                    const int m = wave + 4 * i;
+                    if (!(match >> m & 1)) continue;
+                    float *at = rows + m * a.ldy + n;
+                    if constexpr (YVEC) {
+                        v4f *own = reinterpret_cast<v4f *>(at + 4 * lane);
+                        if (n + 4 * lane < len)
+                            f(i, m, [&](v4f &v) { v = MT > 1 ? __builtin_nontemporal_load(own) : *own; },
+                              [&](const v4f &v) {
+                                  if constexpr (MT > 1) __builtin_nontemporal_store(v, own);
+                                  else *own = v;
+                              });
+                    } else {
+                        f(i, m,
+                          [&](v4f &v) {
+#pragma unroll
+                              for (int e = 0; e < 4; ++e)
+                                  if (n + channel(e) < len) v[e] = at[channel(e)];
+                          },
+                          [&](const v4f &v) {
+#pragma unroll
+                              for (int e = 0; e < 4; ++e)
+                                  if (n + channel(e) < len) at[channel(e)] = v[e];
+                          });
+                    }
+                }
+            };
+            auto read = [&](int i, int, auto get, auto) { get(y[i]); };
+            int n = 0;
+            load_channels(n);  // (in flight while S is summed)
             each_y(n, read);
-            lds_barrier();  // (D has been read)
-        }
-    });
+            if (rank == 0) return;
+            uint4 keep[KS];  // which values of a lane's pieces count
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                keep[s] = keep8(rank - first[s]);
+                if constexpr (!VEC) keep[s] = and8(keep[s], not8(keep8(32 * s + 8 * q - first[s])));
+            }
+            lds_barrier();  // (the rows of the adapter before have been read)
+            const int64_t part = a.M * p.rp;
+            for (int i = threadIdx.x; i < 16 * MT * 8 * KS; i += 256) {
+                const int m = i / (8 * KS), j = i % (8 * KS) * 4;
+                v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+                if ((match >> m & 1) && j < rank) {
+                    const float *src = a.ws + (m0 + m) * p.rp + j;
+                    for (int k = 0; k < p.splits; k += 8) {  // (eight parts' loads at a time)
+                        v4f v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (k + e < p.splits)
+                                v[e] = *reinterpret_cast<const v4f *>(src + (k + e) * part);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (k + e < p.splits) s += v[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = j + e < rank ? s[e] : 0.0f;
+                }
+                *reinterpret_cast<v4f *>(&S[m][j]) = s;
+            }
+            lds_barrier();
+            v8bf f[MT][KS][3];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    float v[8];
+                    const float *src = &S[16 * t + c16][first[s]];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = VEC || first[s] + e >= 32 * s + 8 * q ? src[e] : 0.0f;
+                    cut3(v, f[t][s]);
+                }
+            for (;;) {
+                const int next = n + 64 * NU;
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < KS; ++s)
+#pragma unroll
+                            for (int i = 2; i >= 0; --i)
+                                acc = mfma(__builtin_bit_cast(v8bf, and8(w[u][s], keep[s])), f[t][s][i], acc);
+                        *reinterpret_cast<v4f *>(&D[16 * t + c16][64 * wave + 16 * u + 4 * q]) = acc;
+                    }
+                if (next < len) load_channels(next);
+                lds_barrier();
+                each_y(n, [&](int i, int m, auto, auto put) {
+                    v4f v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(scale, D[m][channel(e)], y[i][e]);
+                    put(v);
+                });
+                if (next >= len) break;
+                n = next;
+                each_y(n, read);
+                lds_barrier();  // (D has been read)
+            }
+        });
     }
 }
 

@@ -73,7 +73,7 @@ def test_codes_against_the_oracle(orc):
     assert (q.cpu().numpy() == qo).all() and (sx.cpu().numpy() == so).all()
 
 
-@pytest.mark.parametrize("K", [64, 72, 4096, 4100, 20000])
+@pytest.mark.parametrize("K", [64, 72, 4096, 4100, 20000, 32767, 40001])
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_in_place_strided_and_shifted(K, dt):
     """The sum over the residual or over x; rows of x that lie apart; operands at
