@@ -107,14 +107,37 @@ class Block:
         return self.output(x, o), q, o
 
     def fork(self, parents, children) -> torch.Tensor:
-        self.adapter[children.long()] = self.adapter[parents.long()]
-        return w4.kv_fork(self.cache, self.table, self.lens, self.refs, parents, children)
+        ok = w4.kv_fork(self.cache, self.table, self.lens, self.refs, parents, children)
+        if self.adapters:
+            hand_on(self.adapter, parents, children, ok)
+        return ok
 
     def free(self, slots) -> None:
         w4.kv_free(self.table, self.lens, self.refs, slots)
+        if self.adapters:
+            drop(self.adapter, slots)
 
     def compact(self) -> torch.Tensor:
         return w4.kv_compact(self.cache, self.table, self.refs)[2]
+
+
+def put(adapter: torch.Tensor, slots: torch.Tensor, on: torch.Tensor, values) -> None:
+    """adapter[slots] = values where `on`; what the other slots name is no matter."""
+    wide = torch.cat([adapter, adapter[:1]])  # (the row behind the last takes the others)
+    wide[torch.where(on, slots, adapter.numel()).long()] = values
+    adapter.copy_(wide[:-1])
+
+
+def hand_on(adapter: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
+            ok: torch.Tensor) -> None:
+    """A granted fork's child has its parent's adapter; a fork that is not granted changes none."""
+    on = ok > 0
+    put(adapter, children, on, adapter[torch.where(on, parents, 0).long()])
+
+
+def drop(adapter: torch.Tensor, slots: torch.Tensor) -> None:
+    """Retired slots name no adapter; slots that there are not are skipped."""
+    put(adapter, slots, (slots >= 0) & (slots < adapter.numel()), -1)
 
 
 def ints(*v) -> torch.Tensor:
