@@ -81,14 +81,14 @@ class Block:
 
     def prompts(self, x: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, layer: int = 0,
                 window: int = 0, sinks: int = 0):
-        """New prompts x [T, hidden] (rows cu[i] : cu[i + 1]) into empty slots; (x', q, o)."""
+        """New prompts x [T, hidden] (rows cu[i] : cu[i + 1], others are padding) into empty
+        slots; (x', q, o)."""
         add = torch.zeros_like(self.lens)
         add[slots.long()] = cu[1:] - cu[:-1]
         ok = self.reserve(add)
         self.lens += add * ok
         table, lens = self.table[slots.long()], self.lens[slots.long()]
-        rows = torch.repeat_interleave(self.adapter[slots.long()], cu[1:] - cu[:-1],
-                                       output_size=x.shape[0]) if self.adapters else None
+        rows = of_rows(self.adapter[slots.long()], cu, x.shape[0]) if self.adapters else None
         q, k, v = self.project(x, rows)
         q = self.append(layer, q, k, v, table, torch.zeros_like(lens), cu)
         o = w4.kv_prefill_attention(q, self.cache, layer, table, lens, cu, window=window, sinks=sinks)
@@ -119,6 +119,14 @@ class Block:
 
     def compact(self) -> torch.Tensor:
         return w4.kv_compact(self.cache, self.table, self.refs)[2]
+
+
+def of_rows(adapter: torch.Tensor, cu: torch.Tensor, T: int) -> torch.Tensor:
+    """Each of T rows' adapter: its sequence's, -1 in rows of no sequence."""
+    t = torch.arange(T, dtype=torch.int32, device=cu.device)
+    b = torch.searchsorted(cu[1:].contiguous(), t, right=True)
+    inside = (t >= cu[0]) & (b < adapter.numel())
+    return torch.where(inside, adapter[b.clamp(max=adapter.numel() - 1)], -1)
 
 
 def put(adapter: torch.Tensor, slots: torch.Tensor, on: torch.Tensor, values) -> None:

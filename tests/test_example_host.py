@@ -34,3 +34,14 @@ def test_retired_slots_name_no_adapter():
     a = ints(4, 1, 7, 2)
     decode_layer.drop(a, ints(2, 0, 2, -1, 4, 2 ** 31 - 1, -2 ** 31))
     assert a.tolist() == [-1, 1, -1, 2]
+
+
+def test_rows_of_a_padded_batch():
+    """Rows before the first sequence and behind the last have no adapter, and
+    sequences of no rows take none."""
+    f = decode_layer.of_rows
+    assert f(ints(7, 3), ints(0, 2, 5), 5).tolist() == [7, 7, 3, 3, 3]
+    assert f(ints(7, 3), ints(1, 2, 4), 6).tolist() == [-1, 7, 3, 3, -1, -1]
+    assert f(ints(7, 3, -1, 5), ints(0, 0, 2, 3, 3), 4).tolist() == [3, 3, -1, -1]
+    assert f(ints(7), ints(2, 2), 3).tolist() == [-1, -1, -1]
+    assert f(ints(7), ints(0, 1), 1).dtype == torch.int32

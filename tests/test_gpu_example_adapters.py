@@ -37,3 +37,30 @@ def test_a_block_without_adapters_forks_as_the_cache_does():
     ex, b = block(0)
     assert b.fork(ex.ints(2, 0, 7), ex.ints(3, -1, 4)).tolist() == [1, 0, 0]
     assert b.lens.tolist() == [20, 0, 30, 30, 0] and b.adapter.tolist() == [-1] * 5
+
+
+def test_a_padded_batch_of_prompts():
+    """Rows of no sequence in front of the prompts and behind them: the prompts have
+    their own adapters, as without the padding."""
+    import int4_weight_quantized_amd as w4
+
+    ex, b = block(3)
+    _, c = block(3)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((40, 256), generator=g, device="cuda")
+    seen = []
+    project = b.project
+
+    def looked(x, adapter=None):
+        seen.append(adapter.tolist())
+        return project(x, adapter)
+    b.project = looked
+    for one in (b, c):
+        one.adapter[1], one.adapter[3] = 2, 1
+    _, q, o = b.prompts(x, ex.ints(3, 1), ex.ints(3, 14, 31))
+    _, r, p = c.prompts(x[3:31].contiguous(), ex.ints(3, 1), ex.ints(0, 11, 28))
+    assert seen == [[-1] * 3 + [1] * 11 + [2] * 17 + [-1] * 9]
+    assert torch.equal(q[3:31], r) and torch.equal(o[3:31], p)
+    for s, n in ((3, 11), (1, 17)):
+        got, want = (w4.kv_gather(t.cache, 0, t.table[s:s + 1].contiguous(), ex.ints(0), ex.ints(0, n), n) for t in (b, c))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
