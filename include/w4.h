@@ -633,7 +633,8 @@ int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, 
 /* Low-rank adapters of many requests at once, beside a product whose weights
  * they share: with a = ids[m],
  *   Y[m][n] += scales[a] * sum_j (sum_k X[m][k] * A[a][j][k]) * B[a][n][j].
- *   X       M rows of K values of x_dtype (kv_x_dtype), x_stride elements apart;
+ *   X       the input of that product (behind a norm: the norm, not what it was taken
+ *           of), M rows of K values of x_dtype (kv_x_dtype), x_stride elements apart;
  *   ids     [M] int32; a row whose id is outside [0, adapters) stays as it is;
  *   A       [adapters][rank][K], B [adapters][N][rank] bf16 bit patterns;
  *   scales  [adapters] fp32, or NULL for ones;

@@ -239,7 +239,8 @@ def lora_add(Y: torch.Tensor, X: torch.Tensor, ids: torch.Tensor, A: torch.Tenso
     """Y[m] += scales[a] (X[m] A[a]^T) B[a]^T with a = ids[m] (outside the pool:
     nothing), in place.
 
-    Y [M, N] fp32 and X [M, K] (bf16 or fp32): rows may lie apart; ids [M] int32;
+    Y [M, N] fp32, a projection's output, and X [M, K] (bf16 or fp32), that projection's
+    own input (behind a norm: the norm): rows may lie apart; ids [M] int32;
     A [adapters, rank, K], B [adapters, N, rank] bf16; scales [adapters] fp32;
     ranks [adapters] int32 where adapters have less than rank."""
     px, ldx = _matrix_rows(X, "X", _XTYPES)
