@@ -643,7 +643,11 @@ int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, 
  *           hold takes no part, NaN included;
  *   Y       M rows of N fp32, y_stride elements apart (the product's output, or
  *           a slice of its columns); it overlaps no other argument.
- * Products of X, A and B keep fp32 accuracy for both types of X, sums are fp32;
+ * Products of X, A and B keep fp32 accuracy for both types of X (bits of fp32 X and of
+ * X A^T below 2^-133 are dropped), sums are fp32.  A NaN or an infinity in X, or an
+ * X A^T beyond fp32, makes its own row's outputs NaN or infinite, one in A or B the
+ * outputs that it reaches; NaN also where the formula has an infinity.  What no row's
+ * adapter uses takes no part;
  * a row's result does not depend on the other rows, nor on their order.  Rows
  * of one adapter that lie next to each other are computed together.
  *   workspace  lora_workspace_bytes(M, K, N, rank) bytes, 256-byte aligned; scratch.
