@@ -647,9 +647,10 @@ int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, 
  * X A^T below 2^-133 are dropped), sums are fp32.  A NaN or an infinity in X, or an
  * X A^T beyond fp32, makes its own row's outputs NaN or infinite, one in A or B the
  * outputs that it reaches; NaN also where the formula has an infinity.  What no row's
- * adapter uses takes no part;
- * a row's result does not depend on the other rows, nor on their order.  Rows
- * of one adapter that lie next to each other are computed together.
+ * adapter uses takes no part.  In calls of the same M, K and rank, and of the same type,
+ * stride and alignment of X and A, a row's result does not depend on the other rows
+ * nor on their order, bit for bit; between those, sums over K are in other parts.
+ * Rows of one adapter that lie next to each other are computed together.
  *   workspace  lora_workspace_bytes(M, K, N, rank) bytes, 256-byte aligned; scratch.
  * 1 <= rank <= 256, 1 <= adapters <= 2^20, 1 <= M <= 2^23, 1 <= K <= W4_MAX_K,
  * 1 <= N < 2^31, adapters * rank * max(K, N) <= 2^46.

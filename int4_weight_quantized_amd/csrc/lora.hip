@@ -6,7 +6,8 @@
 // different adapters that its tile names (a ballot over the tile's ids; slots of
 // workgroups share them out) and computes the tile's rows of one adapter at a
 // time, so that no plan, no sorting and no atomics are needed and a row's result
-// does not depend on its neighbours.
+// does not depend on its neighbours (but on M: with it change the parts of K, whose
+// sums are added in their order).
 //
 // Products are bf16 MFMAs (16 x 16 x 32) with fp32 sums.  An fp32 value of X, and
 // every value of S, is three bf16 terms of 8 bits each, cut off one after the
