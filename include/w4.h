@@ -544,8 +544,10 @@ typedef enum { RMS_BF16 = 0, RMS_FP32 = 1 } rms_dtype;
  *            residual itself, or x itself where x_stride is K;
  *   out      [M][K] of out_dtype; it overlaps nothing else.
  * eps is finite and not below 0.  1 <= K <= W4_MAX_K, 1 <= M <= 2^23, M * K <= 2^36.
- * Since h^2 is exact in fp64 and the mean is rounded far below fp32, the result
- * does not depend on the order of the sum: every kernel gives the same bits.
+ * h^2 is exact in fp64 and the mean is rounded far below fp32, so that r is fl of the
+ * formula's value except where that lies within a few fp64 roundings of the middle
+ * between two fp32 values (about one row in 2^27): there it is either of them, by the
+ * order of the sum, which is the same in calls of the same K, type of x, and alignment.
  * A row with a value that is not finite gives what the formula gives for it
  * (NaN, or 0 beside an infinity); other rows are not touched by it.  A row of
  * zeros with eps 0 is NaN.
@@ -555,7 +557,8 @@ int rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *residual,
              void *out, int out_dtype, void *stream);
 
 /* The same with int8 rows as w4a8_linear_q takes them: Xq [M][K] and sx [M] are
- * bit for bit those that a8_quantize_act makes of rms_norm's fp32 output.  A row
+ * bit for bit those that a8_quantize_act makes of rms_norm's fp32 output (of one with
+ * the same r, see there: all calls whose operands are aligned to 16 bytes).  A row
  * whose output has a value that is not finite gets the scale NaN (its codes are
  * then unspecified), so that a product of it is NaN.
  * (For awq_quantize_act of the output, pass fl(offset + weight) / s and offset 0:

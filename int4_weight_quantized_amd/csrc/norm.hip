@@ -4,8 +4,10 @@
 //   sx = fl(max |y| / 127), code = clamp(rne(fl(y / sx)), -128, 127).
 // A square of fp32 is exact in fp64 and the sum's rounding there lies 2^-29
 // below fp32's, so r, and with it every code next to a rounding border, is the
-// same whichever way a row is split over lanes.  Bound by memory: a row is read
-// once, kept in registers between the sum and the output, and written once.
+// same whichever way a row is split over lanes, but for a row in about 2^27 whose
+// 1 / sqrt(...) lies in the middle between two fp32 values to within that rounding.
+// Bound by memory: a row is read once, kept in registers between the sum and the
+// output, and written once.
 #include <type_traits>
 
 #include "kv_common.h"
