@@ -4,8 +4,9 @@
 //   (a, b) -> (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))),
 //   c, s = fp32 of magnitude * cos, sin(2 pi t).
 // Angles are taken in fp64: p turns[i] loses 2^-53 of itself, so that a token at
-// position 10^6 still has its angle to 10^-10 where fp32 would be off by a tenth
-// of a turn, and c and s are rounded once.
+// position 10^6 still has its angle to 10^-10 where fp32 would be off by a hundredth
+// of a turn (0.013 at base 10000, nearly a tenth of a radian), and c and s are rounded
+// once.
 //
 // A wave takes one token: it computes the token's angles (64 at once), keeps those
 // of its lanes' values in registers, and goes through the token's heads, 1 KB at a
