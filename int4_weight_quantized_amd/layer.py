@@ -122,10 +122,15 @@ def a8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
-                     factor: float = 1.0, context: int = 0, fast: float = 32.0, slow: float = 1.0):
-    """(turns a token of each pair, float64 [rot_dim / 2] in host memory, magnitude)."""
+                     factor: float = 1.0, context: int = 0, fast: float = None, slow: float = 1.0):
+    """(turns a token of each pair, float64 [rot_dim / 2] in host memory, magnitude).
+
+    fast, slow: turns within the context that bound the ramp of "yarn" (None: 32 to 1) and
+    "bands" (None: 4 to 1), the values that models use."""
     if scaling not in _SCALINGS:
         raise ValueError(f"unknown scaling {scaling!r} ({', '.join(_SCALINGS)})")
+    if fast is None:
+        fast = 4.0 if scaling == "bands" else 32.0
     turns = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
     magnitude = _D()
     _check("rope_frequencies", lib().rope_frequencies(
@@ -139,10 +144,10 @@ class Rope:
 
     layout "half": pairs (i, i + rot_dim / 2); "pairs": (2 i, 2 i + 1).
     scaling, factor, context, fast, slow: how frequencies are stretched beyond a
-    trained context (``rope_scaling`` in w4.h)."""
+    trained context (``rope_scaling`` in w4.h, ``rope_frequencies``)."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half",
-                 scaling: str = "none", factor: float = 1.0, context: int = 0, fast: float = 32.0,
+                 scaling: str = "none", factor: float = 1.0, context: int = 0, fast: float = None,
                  slow: float = 1.0, device="cuda"):
         turns, magnitude = rope_frequencies(rot_dim, base, scaling, factor, context, fast, slow)
         self._init(turns.to(device), layout, magnitude)
