@@ -131,7 +131,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
         raise ValueError(f"unknown scaling {scaling!r} ({', '.join(_SCALINGS)})")
     if fast is None:
         fast = 4.0 if scaling == "bands" else 32.0
-    turns = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    turns = torch.empty(min(max(rot_dim // 2, 1), 256), dtype=torch.float64)  # (512 at most are taken)
     magnitude = _D()
     _check("rope_frequencies", lib().rope_frequencies(
         rot_dim, base, _SCALINGS[scaling], factor, context, fast, slow, turns.data_ptr(),

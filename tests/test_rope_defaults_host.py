@@ -23,3 +23,10 @@ def test_bands_share_of_each_pair():
         turns = 2048 * a
         keep = min(max((turns - 1) / 3, 0.0), 1.0)
         assert b == pytest.approx(a * (keep + (1 - keep) / 8), rel=1e-12)
+
+
+@pytest.mark.parametrize("rot", [-2, 0, 7, 514, 1 << 45])
+def test_sizes_are_refused_before_memory_is_taken(rot):
+    with pytest.raises(w4.W4Error):
+        w4.rope_frequencies(rot)
+    assert w4.rope_frequencies(512)[0].shape == (256,)
