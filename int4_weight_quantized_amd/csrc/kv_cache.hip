@@ -11,8 +11,8 @@ namespace w4 {
 // A group of LPV lanes (8, 16 or 32: head_dim up to 64, 128, 256) handles one
 // head's vector of one token, 8 values a lane; blockIdx.y selects K or V.
 // Bound by memory: each value is read once and written once (179 MB of prompts, 8
-// heads of 128, bf16: 42 us, 4.2 TB/s; a large copy: 4.9; 224 MB of fp32 to int8: 60
-// us).  The row's values are loaded before the search for its sequence, and stored past
+// heads of 128, bf16: 42 us, 4.2 TB/s; a large copy: 4.9; 224 MB of fp32 to int8: 58
+// us, 72 with a division a value).  The row's values are loaded before the search for its sequence, and stored past
 // the caches.
 
 struct KvPlace {
@@ -51,6 +51,33 @@ __device__ __forceinline__ KvPlace kv_place(const KvView &c, const KvRows &r) {
     return p;
 }
 
+template <bool FP32>
+__device__ __forceinline__ void load8(const void *x, int64_t at, bool vec, float (&f)[8]) {
+    if constexpr (FP32) {
+        const float *s = reinterpret_cast<const float *>(x) + at;
+        if (vec) {
+            const float4 a = *reinterpret_cast<const float4 *>(s);
+            const float4 b = *reinterpret_cast<const float4 *>(s + 4);
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = s[j];
+        }
+    } else {
+        const uint16_t *s = reinterpret_cast<const uint16_t *>(x) + at;
+        if (vec) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(s);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float((uint32_t)s[j] << 16);
+        }
+    }
+}
+
 template <bool INT8, bool FP32, int LPV>
 __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const void *k,
                                                    const void *v, int64_t ldk, int64_t ldv,
@@ -65,7 +92,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvView c, KvRows r, const voi
                     f);
     }
     const KvPlace p = kv_place<LPV>(c, r);
-    kv_store8<INT8, LPV>(c, isv, p.vec, d, p.vec >= 0 && d < c.D, f);
+    kv_store<INT8, 8, LPV>(c, isv, p.vec, d, p.vec >= 0 && d < c.D, f);
 }
 
 template <bool INT8, bool FP32, int LPV>

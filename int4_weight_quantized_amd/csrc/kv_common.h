@@ -41,62 +41,52 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
 
-template <bool FP32>
-__device__ __forceinline__ void load8(const void *x, int64_t at, bool vec, float (&f)[8]) {
-    if constexpr (FP32) {
-        const float *s = reinterpret_cast<const float *>(x) + at;
-        if (vec) {
-            const float4 a = *reinterpret_cast<const float4 *>(s);
-            const float4 b = *reinterpret_cast<const float4 *>(s + 4);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = s[j];
-        }
-    } else {
-        const uint16_t *s = reinterpret_cast<const uint16_t *>(x) + at;
-        if (vec) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(s);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float((uint32_t)s[j] << 16);
-        }
-    }
-}
-
-// Rounding to the cache's type happens once, here: bf16 half to even, or int8 with
-// the scale absmax * fl(1 / 127) of the head's vector (one multiplication, within
-// one unit in the last place of the quotient) and codes rne(fl(x / scale)).  A
+// A head's vector into its place; rounding to the cache's type happens once, here:
+// bf16 half to even, or int8 with the scale absmax * fl(1 / 127) of the vector (one
+// multiplication, within one unit in the last place of the quotient) and codes
+// rne(fl(x / scale)), whose quotients are correctly rounded without a division.  A
 // vector with a value that is not finite has no int8 form: its scale is NaN.
-// `on`: this lane has values of a vector with a place; LPV lanes share a vector.
-template <bool INT8, int LPV>
-__device__ __forceinline__ void kv_store8(const KvView &c, bool isv, int64_t vec, int d, bool on,
-                                          const float (&f)[8]) {
+// LPV lanes share a vector, V values a lane (d: the lane's first); `on`: this lane has
+// values of a vector with a place.
+template <bool INT8, int V, int LPV>
+__device__ __forceinline__ void kv_store(const KvView &c, bool isv, int64_t vec, int d, bool on,
+                                         const float (&f)[V]) {
     uint8_t *pool = isv ? c.v : c.k;
     if constexpr (INT8) {
         // the bits of |x| order as the values do, infinity and NaN above them all
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        m = max(m, (uint32_t)dpp<kQuadSwap1>((int)m));
+        m = max(m, (uint32_t)dpp<kQuadSwap2>((int)m));
+        m = max(m, (uint32_t)dpp<kRowHalfMirror>((int)m));
+        if constexpr (LPV > 8) m = max(m, (uint32_t)dpp<kRowMirror>((int)m));
 #pragma unroll
-        for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
+        for (int o = 16; o < LPV; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
         if (!on) return;
         const float s = m < 0x7F800000u ? __uint_as_float(m) * (1.0f / 127.0f) : NAN;
-        uint32_t w[2] = {};
+        uint32_t w[V / 4] = {};
+        auto codes = [&](auto code) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j / 4] |= (uint32_t)(quant_code(f[j], s, -128.0f, 127.0f) & 0xFF) << (j % 4 * 8);
-        *reinterpret_cast<uint2 *>(pool + vec * c.D + d) = uint2{w[0], w[1]};
+            for (int i = 0; i < V / 4; ++i)
+                w[i] = pack4_i8(code(f[4 * i]), code(f[4 * i + 1]), code(f[4 * i + 2]), code(f[4 * i + 3]));
+        };
+        if (s >= kFastQuotientMinScale) {
+            const float rs = 1.0f / s;
+            codes([&](float x) { return (int)code_in_low_byte(quotient_rn(x, s, rs)); });
+        } else {  // zero, tiny or NaN
+            codes([&](float x) { return quant_code(x, s, -128.0f, 127.0f); });
+        }
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(pool + vec * c.D + d) = uint2{w[0], w[1]};
+        else *reinterpret_cast<uint32_t *>(pool + vec * c.D + d) = w[0];
         if (d == 0) (isv ? c.vs : c.ks)[vec] = s;
     } else {
         if (!on) return;
-        const u32x4 o = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7])};
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(pool + (vec * c.D + d) * 2));
+        typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+        words w;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+        __builtin_nontemporal_store(w, reinterpret_cast<words *>(pool + (vec * c.D + d) * 2));
     }
 }
 

@@ -261,50 +261,6 @@ __device__ __forceinline__ TokenPlace token_place(const KvView &c, const KvRows 
                           : (((int64_t)page * c.heads) << c.shift) + (pos & ((1 << c.shift) - 1))};
 }
 
-// A head's vector into its place: bf16 half to even, or int8 by the cache's rule
-// (scale = absmax * fl(1 / 127), NaN for a vector that is not finite; the codes'
-// quotients are kv_store8's, correctly rounded without a division).
-template <bool INT8, int V, int LPV>
-__device__ __forceinline__ void cache_values(const KvView &c, bool isv, int64_t vec, int d, bool on,
-                                             const float (&f)[V]) {
-    uint8_t *pool = isv ? c.v : c.k;
-    if constexpr (INT8) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-        m = max(m, (uint32_t)dpp<kQuadSwap1>((int)m));
-        m = max(m, (uint32_t)dpp<kQuadSwap2>((int)m));
-        m = max(m, (uint32_t)dpp<kRowHalfMirror>((int)m));
-        if constexpr (LPV > 8) m = max(m, (uint32_t)dpp<kRowMirror>((int)m));
-#pragma unroll
-        for (int o = 16; o < LPV; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
-        if (!on) return;
-        const float s = m < 0x7F800000u ? __uint_as_float(m) * (1.0f / 127.0f) : NAN;
-        uint32_t w[V / 4] = {};
-        auto codes = [&](auto code) {
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i)
-                w[i] = pack4_i8(code(f[4 * i]), code(f[4 * i + 1]), code(f[4 * i + 2]), code(f[4 * i + 3]));
-        };
-        if (s >= kFastQuotientMinScale) {
-            const float rs = 1.0f / s;
-            codes([&](float x) { return (int)code_in_low_byte(quotient_rn(x, s, rs)); });
-        } else {  // zero, tiny or NaN
-            codes([&](float x) { return quant_code(x, s, -128.0f, 127.0f); });
-        }
-        if constexpr (V == 8) *reinterpret_cast<uint2 *>(pool + vec * c.D + d) = uint2{w[0], w[1]};
-        else *reinterpret_cast<uint32_t *>(pool + vec * c.D + d) = w[0];
-        if (d == 0) (isv ? c.vs : c.ks)[vec] = s;
-    } else {
-        if (!on) return;
-        typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-        words w;
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-        __builtin_nontemporal_store(w, reinterpret_cast<words *>(pool + (vec * c.D + d) * 2));
-    }
-}
-
 // The pieces of a token are those of its queries, then of its keys, then of its
 // values, each kind a whole number of pieces.
 template <bool INT8, bool FP32, int MODE, int V, int LPV>
@@ -362,8 +318,8 @@ __global__ __launch_bounds__(256) void k_kv_append_rope(AppendRopeArgs a, int pa
             } else if (place.at >= 0) {
                 const bool isv = n >= nq + nk;
                 const int h = (isv ? n - nq - nk : n - nq) * Row::kHeads + lane / LPV;
-                cache_values<INT8, V, LPV>(a.c, isv, place.at + ((int64_t)h << a.c.shift), d,
-                                           h < heads && d < D, f);
+                kv_store<INT8, V, LPV>(a.c, isv, place.at + ((int64_t)h << a.c.shift), d,
+                                       h < heads && d < D, f);
             }
         }
     }
