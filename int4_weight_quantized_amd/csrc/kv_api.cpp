@@ -143,8 +143,8 @@ w4::KvView w4::kv_layer_view(const kv_cache *c, int64_t layer, const int32_t *ta
 
 // Checks shared by kv_append, kv_gather and kv_append_rope (strides in elements).
 int w4::check_kv_rows(const kv_cache *c, int64_t layer, const void *k, const void *v, int x_dtype,
-               int64_t ldk, int64_t ldv, int64_t T, int64_t B, const int32_t *table, int64_t W,
-               const int32_t *start, const int32_t *cu, size_t align) {
+                      int64_t ldk, int64_t ldv, int64_t T, int64_t B, const int32_t *table,
+                      int64_t W, const int32_t *start, const int32_t *cu, size_t align) {
     int rc = check_cache(c);
     if (rc != W4_OK) return rc;
     if (!k || !v || !start) return W4_ERR_NULL;
@@ -165,8 +165,8 @@ extern "C" {
 int kv_append(const kv_cache *cache, int64_t layer, const void *k, const void *v, int x_dtype,
               int64_t k_stride, int64_t v_stride, int64_t T, int64_t B, const int32_t *table,
               int64_t W, const int32_t *start, const int32_t *cu, void *stream) {
-    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, k_stride, v_stride, T, B, table, W,
-                              start, cu, x_dtype == KV_X_FP32 ? 4 : 2);
+    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, k_stride, v_stride, T, B, table,
+                                     W, start, cu, x_dtype == KV_X_FP32 ? 4 : 2);
     if (rc != W4_OK) return rc;
     const w4::KvRows rows{start, cu, T, B};
     return w4::finish_call(
@@ -180,8 +180,8 @@ int kv_gather(const kv_cache *cache, int64_t layer, void *k, void *v, int x_dtyp
               int64_t B, const int32_t *table, int64_t W, const int32_t *start,
               const int32_t *cu, void *stream) {
     const int64_t row = cache ? cache->heads * cache->head_dim : 0;
-    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, row, row, T, B, table, W, start, cu,
-                              16);
+    const int rc = w4::check_kv_rows(cache, layer, k, v, x_dtype, row, row, T, B, table, W, start,
+                                     cu, 16);
     if (rc != W4_OK) return rc;
     const w4::KvRows rows{start, cu, T, B};
     return w4::finish_call(
