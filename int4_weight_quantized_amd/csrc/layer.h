@@ -27,7 +27,7 @@ struct NormArgs {
 };
 constexpr int kNormInt8 = 2;
 
-// `path`: the kernel variant taken.
+// `path`, here and below: the kernel variant taken.
 hipError_t launch_rms_norm(const NormArgs &a, const char **path, hipStream_t st);
 
 // Frequencies of a rotation and where it applies (rope_spec).
@@ -49,7 +49,7 @@ struct RopeArgs {
     int64_t ldo;
 };
 
-hipError_t launch_rope(const RopeArgs &a, hipStream_t st);
+hipError_t launch_rope(const RopeArgs &a, const char **path, hipStream_t st);
 
 struct AppendRopeArgs {
     RopeView rope;
@@ -64,7 +64,7 @@ struct AppendRopeArgs {
     int64_t ldo;
 };
 
-hipError_t launch_kv_append_rope(const AppendRopeArgs &a, hipStream_t st);
+hipError_t launch_kv_append_rope(const AppendRopeArgs &a, const char **path, hipStream_t st);
 
 struct LoraArgs {
     const void *X;

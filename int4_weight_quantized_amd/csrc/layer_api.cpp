@@ -149,7 +149,9 @@ int rope_rotate(const rope_spec *rope, const void *x, int x_dtype, int64_t x_str
         return W4_ERR_ALIGN;
     const w4::RopeArgs a{rope_view(rope), x, x_dtype == KV_X_FP32, x_stride, T, (int)heads,
                          (int)head_dim, pos, out, out_stride};
-    return w4::finish_call("rope_rotate", w4::launch_rope(a, hip_stream(stream)));
+    const char *path = "none";
+    const hipError_t e = w4::launch_rope(a, &path, hip_stream(stream));
+    return w4::finish_call(path, e);
 }
 
 int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, const void *q,
@@ -178,7 +180,9 @@ int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, 
                                q_stride, k_stride, v_stride,
                                (int)q_heads,
                                q_out, out_stride};
-    return w4::finish_call("kv_append_rope", w4::launch_kv_append_rope(a, hip_stream(stream)));
+    const char *path = "none";
+    const hipError_t e = w4::launch_kv_append_rope(a, &path, hip_stream(stream));
+    return w4::finish_call(path, e);
 }
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank) {

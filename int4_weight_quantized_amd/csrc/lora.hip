@@ -566,7 +566,7 @@ static void go_up(const LoraArgs &a, const LoraPlan &p, hipStream_t st) {
 }
 
 template <int MT>
-static void go(const LoraArgs &a, hipStream_t st) {
+static void go(const LoraArgs &a, const char **path, hipStream_t st) {
     auto at16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     const int64_t tiles = (a.M + 16 * MT - 1) / (16 * MT);
     // Workgroups of a tile: as many as its adapters can use, or 2048 of the call.  Their
@@ -603,15 +603,18 @@ static void go(const LoraArgs &a, hipStream_t st) {
     p.slots = slots(tiles * ((a.N + p.nc - 1) / p.nc));
     if (bv) yv ? go_up<true, true, MT>(a, p, st) : go_up<true, false, MT>(a, p, st);
     else yv ? go_up<false, true, MT>(a, p, st) : go_up<false, false, MT>(a, p, st);
+    // (the operands that are not taken in aligned pieces; X's includes A's)
+    static const char *const kPaths[] = {"lora",       "lora_odd_x",  "lora_odd_b",  "lora_odd_xb",
+                                         "lora_odd_y", "lora_odd_xy", "lora_odd_by", "lora_odd_xby"};
+    *path = kPaths[(xv ? 0 : 1) + (bv ? 0 : 2) + (yv ? 0 : 4)];
 }
 
 hipError_t launch_lora(const LoraArgs &a, const char **path, hipStream_t st) {
-    *path = "lora";
     // Tiles of 32 rows halve the traffic of A and B, of 16 spread a step's adapters over
     // more workgroups (8192 rows, first launch, 32 / 16: 33 / 37 us); more than 128 ranks
     // of 32 rows would not fit the registers.
-    if (a.M <= 256 || a.rank > 128) go<1>(a, st);
-    else go<2>(a, st);
+    if (a.M <= 256 || a.rank > 128) go<1>(a, path, st);
+    else go<2>(a, path, st);
     return hipGetLastError();
 }
 

@@ -347,9 +347,10 @@ static void by_head(int D, F f) {
 }
 
 template <bool FP32>
-static void go_rope(const RopeArgs &a, hipStream_t st) {
+static void go_rope(const RopeArgs &a, const char **path, hipStream_t st) {
     const bool vec = aligned16(a.x, a.ldx, FP32) && aligned16(a.out, a.ldo, FP32);
     const bool lines = a.D * (FP32 ? 4 : 2) % 128 == 0;
+    *path = !vec ? "rope_rotate_odd" : !lines ? "rope_rotate_cached" : "rope_rotate";
     by_head<FP32>(a.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value;
         const int parts = parts_of(a.T, (a.heads + kWave / LPV - 1) / (kWave / LPV));
@@ -360,17 +361,18 @@ static void go_rope(const RopeArgs &a, hipStream_t st) {
     });
 }
 
-hipError_t launch_rope(const RopeArgs &a, hipStream_t st) {
-    if (a.fp32) go_rope<true>(a, st);
-    else go_rope<false>(a, st);
+hipError_t launch_rope(const RopeArgs &a, const char **path, hipStream_t st) {
+    if (a.fp32) go_rope<true>(a, path, st);
+    else go_rope<false>(a, path, st);
     return hipGetLastError();
 }
 
 template <bool INT8, bool FP32>
-static void go_append(const AppendRopeArgs &a, hipStream_t st) {
+static void go_append(const AppendRopeArgs &a, const char **path, hipStream_t st) {
     const bool vec = aligned16(a.q, a.ldq, FP32) && aligned16(a.out, a.ldo, FP32) &&
                      aligned16(a.k, a.ldk, FP32) && aligned16(a.v, a.ldv, FP32);
     const bool lines = a.c.D * (FP32 ? 4 : 2) % 128 == 0;
+    *path = !vec ? "kv_append_rope_odd" : !lines ? "kv_append_rope_cached" : "kv_append_rope";
     by_head<FP32>(a.c.D, [&](auto v, auto lanes) {
         constexpr int V = decltype(v)::value, LPV = decltype(lanes)::value, H = kWave / LPV;
         const int parts = parts_of(a.rows.T, (a.hq + H - 1) / H + 2 * ((a.c.heads + H - 1) / H));
@@ -381,9 +383,9 @@ static void go_append(const AppendRopeArgs &a, hipStream_t st) {
     });
 }
 
-hipError_t launch_kv_append_rope(const AppendRopeArgs &a, hipStream_t st) {
-    if (a.int8) a.fp32 ? go_append<true, true>(a, st) : go_append<true, false>(a, st);
-    else a.fp32 ? go_append<false, true>(a, st) : go_append<false, false>(a, st);
+hipError_t launch_kv_append_rope(const AppendRopeArgs &a, const char **path, hipStream_t st) {
+    if (a.int8) a.fp32 ? go_append<true, true>(a, path, st) : go_append<true, false>(a, path, st);
+    else a.fp32 ? go_append<false, true>(a, path, st) : go_append<false, false>(a, path, st);
     return hipGetLastError();
 }
 
