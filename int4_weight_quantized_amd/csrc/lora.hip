@@ -595,10 +595,15 @@ static void go(const LoraArgs &a, const char **path, hipStream_t st) {
     // Channels of a workgroup: 256, and more where there are workgroups enough, since each
     // sums S and splits it once (us for 256 / 512 / 1024 / 2048: 64 rows -> 11008, rank 16, 13.8 /
     // 10.7 / 8.6 / 10.0; 16 rows -> 28672, rank 64, 24 / 18 / 13.5 / 13.8; 8192 rows -> 4096, both
-    // launches, 90 / 85 / 92; one row -> 6912 3.5 / 3.8 / 4.7).
-    const int64_t chunks = (a.N + 255) / 256;
-    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(
-        MT == 1 ? 4 : 2, tiles * std::min<int64_t>(16 * MT, a.adapters) * chunks / 448));
+    // launches, 90 / 85 / 92; one row -> 6912 3.5 / 3.8 / 4.7).  As many as leave two workgroups
+    // a CU, 512 in all: beyond them is another round (16 rows of 16 adapters, rank 64, us for
+    // 256 / 512 / 768 / 1024: 544 workgroups of 256 channels 9.3 / 7.1 / 7.6 / 8.4; 1024 11.9 /
+    // 7.7 / 9.2 / 9.0; 1056 14.2 / 12.5 / 9.3 / 10.7; 1552 19.5 / 14.3 / 14.5 / 11.9); four a CU
+    // in tiles of 32 rows, whose slots mostly find no adapter and end (300 rows, 8 adapters, 640
+    // workgroups 4.8 / 7.0, 1280 7.5 / 7.2).
+    const int64_t chunks = (a.N + 255) / 256, full = 512 * MT;
+    const int64_t work = tiles * std::min<int64_t>(16 * MT, a.adapters) * chunks;
+    const int64_t per = std::min<int64_t>(MT == 1 ? 4 : 2, (work + full - 1) / full);
     p.nc = (int)(256 * per);
     p.slots = slots(tiles * ((a.N + p.nc - 1) / p.nc));
     if (bv) yv ? go_up<true, true, MT>(a, p, st) : go_up<true, false, MT>(a, p, st);
