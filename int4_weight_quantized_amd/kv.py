@@ -63,10 +63,17 @@ from . import _check, _dev, _opt, _stream as _stream_handle, lib  # noqa: E402  
 
 def _stream(stream, dev) -> int:
     """Handle of `stream`, or of the current stream of the call's device
-    (without the Stream object of torch.cuda.current_stream, 2.7 us a call)."""
+    (without the Stream object of torch.cuda.current_stream, 2.7 us a call).  The
+    default stream has no handle of its own: it is the current device's, where operands
+    of another one are not to be touched."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return _stream_handle(stream)
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        handle = _stream_handle(stream)
+    if not handle and dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the call's operands are on {dev}, the default stream is the current device's: "
+                         "make theirs current (torch.cuda.device)")
+    return handle
 
 
 def _ptr(t, name, dtype, shape, dev) -> int:
