@@ -653,7 +653,8 @@ int kv_append_rope(const kv_cache *cache, int64_t layer, const rope_spec *rope, 
  * adapter uses takes no part.  In calls of the same M, K and rank, and of the same type,
  * stride and alignment of X and A, a row's result does not depend on the other rows
  * nor on their order, bit for bit; between those, sums over K are in other parts.
- * Rows of one adapter that lie next to each other are computed together.
+ * Rows of one adapter that lie next to each other are computed together, which counts in
+ * calls of more than 256 rows.
  *   workspace  lora_workspace_bytes(M, K, N, rank) bytes, 256-byte aligned; scratch.
  * 1 <= rank <= 256, 1 <= adapters <= 2^20, 1 <= M <= 2^23, 1 <= K <= W4_MAX_K,
  * 1 <= N < 2^31, adapters * rank * max(K, N) <= 2^46.
